@@ -251,6 +251,109 @@ moe_status moe_expert_ffn_q8(const void* x_perm, const int32_t* offsets, const i
                              int I, moe_swiglu act, moe_fc1_layout fc1_layout, void* y_perm,
                              void* workspace, size_t ws_bytes, void* stream);
 
+/* ------------------------------------------- int8 activations x int8 expert weights */
+
+/* Rows to int8, one float32 scale per row (symmetric, per token):
+ *   scale[r] = max_k |x[r, k]| / 127 (float32 division)
+ *   q[r, k]  = 127 x[r, k] / max_k |x[r, k]| to the nearest whole number, ties to even
+ * exactly (the whole number of the real quotient, for every input).  A row of zeros has
+ * scale 0 and q = 0; a row holding an infinity or a NaN has scale NaN and q = 0, so that
+ * its products are NaN.
+ *   x [rows, K] dt, K a multiple of 8; q [rows, K] int8 out; scale [rows] float32 out.
+ * rows = 0 is a no-op. */
+moe_status moe_quantize_rows(const void* x, int rows, int K, moe_dtype dt, int8_t* q, float* scale,
+                             void* stream);
+
+/* Product of int8 rows and int8 weights with a scale per row and per output channel,
+ * grouped by expert or dense:
+ *   out[r, n] = (sum_k a_q[r, k] w_q[e, n, k]) a_scale[r] w_scale[e, n] + bias[e, n]
+ * for the rows r = offsets[e] .. offsets[e+1]-1 of expert e.  The sum is exact (int32).
+ *   a_q [rows, K] int8, a_scale [rows] float32 (moe_quantize_rows)
+ *   w_q [E, N, K] int8, w_scale [E, N] float32
+ *   bias     [E, N] out_dt or NULL
+ *   offsets  [E+1] int32 (device) as in moe_expert_ffn, or NULL: a dense product (E = 1)
+ *   out      [rows, N] out_dt (MOE_BF16 or MOE_F32); rows at or beyond offsets[E] are not
+ *            written
+ *   err_word int32 device word or NULL: MOE_DEVERR_BAD_EXPERT is OR-ed in for offsets that
+ *            decrease or leave [0, rows] (they are clamped), MOE_DEVERR_TIMEOUT for a
+ *            bounded wait that ran out; never cleared here
+ * K a multiple of 16 and at most 65536, N a multiple of 32.  rows = 0 is a no-op. */
+moe_status moe_matmul_q8(const int8_t* a_q, const float* a_scale, const int8_t* w_q,
+                         const float* w_scale, const void* bias, const int32_t* offsets, int rows,
+                         int K, int E, int N, moe_dtype out_dt, void* out, int32_t* err_word,
+                         void* stream);
+
+/* Grouped expert FFN with int8 activations and int8 weights, for any number of rows per
+ * expert (moe_expert_ffn_q8 keeps the activations in bf16 and takes decode batches only):
+ *   x_perm rows to int8 -> product with fc1_q -> SwiGLU in float32 -> activation rows to
+ *   int8 -> product with fc2_q -> y_perm in bf16
+ * each step as in moe_quantize_rows and moe_matmul_q8; the activations are not rounded
+ * between the SwiGLU and their int8.
+ *   x_perm [rows, H] bf16, offsets [E+1]; fc1_q [E, 2I, H] int8 and fc1_scale [E, 2I] in
+ *   fc1_layout, fc2_q [E, H, I] and fc2_scale [E, H]; fc1_bias [E, 2I], fc2_bias [E, H]
+ *   bf16 or NULL; y_perm [rows, H] bf16, rows at or beyond offsets[E] not written
+ *   workspace at least moe_expert_ffn_w8a8_workspace_size(rows, H, E, I) bytes, 256-byte
+ *   aligned, any contents; its first word is the call's device error word.
+ * H and I multiples of 32, at most 65536. */
+size_t moe_expert_ffn_w8a8_workspace_size(int rows, int H, int E, int I);
+moe_status moe_expert_ffn_w8a8(const void* x_perm, const int32_t* offsets, const int8_t* fc1_q,
+                               const float* fc1_scale, const int8_t* fc2_q, const float* fc2_scale,
+                               const void* fc1_bias, const void* fc2_bias, int rows, int H, int E,
+                               int I, moe_swiglu act, moe_fc1_layout fc1_layout, void* y_perm,
+                               void* workspace, size_t ws_bytes, void* stream);
+
+/* The whole layer on moe_expert_ffn_w8a8: [pre-FFN RMSNorm ->] route (on the bf16 input)
+ * -> permute -> int8 expert FFN -> combine.  Arguments as moe_forward_q8; any batch size.
+ * workspace >= moe_w8a8_workspace_size(T, H, E, k, I) bytes, 256-byte aligned; its first
+ * word is the device error word. */
+size_t moe_w8a8_workspace_size(int T, int H, int E, int k, int I);
+moe_status moe_forward_w8a8(const void* hidden, const void* norm_weight, float norm_eps,
+                            const void* router_w, const float* router_bias, const int8_t* fc1_q,
+                            const float* fc1_scale, const int8_t* fc2_q, const float* fc2_scale,
+                            const void* fc1_bias, const void* fc2_bias, int T, int H, int E, int k,
+                            int I, int normalize, moe_swiglu act, moe_fc1_layout fc1_layout,
+                            void* out, void* workspace, size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------ load balance */
+
+/* Load-balance loss of a routing, and the counts it is made of.  The batch is cut into S
+ * sequences (seq_offsets; NULL: the whole batch is one, S = 1).  With n the valid tokens
+ * of a sequence, p_t = softmax(logits_t) over the E experts and c_e the number of its
+ * (token, slot) pairs routed to e:
+ *   f_e = c_e / (n k),  P_e = (1/n) sum_t p_te,  loss = (coef / S) sum_s E sum_e f_e P_e
+ * A sequence without valid tokens adds 0.  Balanced experts give coef.
+ *   logits      [T, E] float32 (moe_route's), topk_idx [T, k] int32 (moe_route's)
+ *   mask        [T] bytes or NULL: 0 marks a token (padding) that takes no part; its
+ *               logits and ids are not read
+ *   seq_offsets [S+1] int32 (device) or NULL: tokens seq_offsets[s] .. seq_offsets[s+1]-1
+ *               are sequence s; non-decreasing, seq_offsets[0] = 0, seq_offsets[S] <= T;
+ *               tokens behind the last sequence take no part
+ *   loss [1], counts [S, E] int32, probs [S, E] float32 (P), tokens [S] int32 (n): out
+ *   err_word    int32 device word or NULL: MOE_DEVERR_BAD_EXPERT is OR-ed in for an id
+ *               outside [0, E) (it is left out of the counts) or bad sequence offsets
+ *               (clamped to [0, T])
+ *   workspace   at least moe_balance_loss_workspace_size(T, E, S) bytes, 256-byte aligned,
+ *               any contents
+ * A logit of -infinity has probability 0; a token whose logits are all -infinity has no
+ * probabilities (0 each) and no gradient, but still counts.  NaN and +infinity propagate.
+ * The results do not depend on the order of anything: the same bits on every call. */
+size_t moe_balance_loss_workspace_size(int T, int E, int S);
+moe_status moe_balance_loss(const float* logits, const int32_t* topk_idx, const uint8_t* mask,
+                            const int32_t* seq_offsets, int T, int E, int k, int S, float coef,
+                            float* loss, int32_t* counts, float* probs, int32_t* tokens,
+                            int32_t* err_word, void* workspace, size_t ws_bytes, void* stream);
+
+/* Gradient of that loss with respect to the logits, the counts being constants:
+ *   dlogits[t, e] = g (coef E / (S n)) p_te (f_e - sum_j f_j p_tj)
+ * with g the gradient arriving at the loss (grad_loss, one float32 on the device, or NULL
+ * for 1).  counts and tokens as moe_balance_loss gave them for the same logits, mask and
+ * sequences.  dlogits [T, E] float32 out, every row written: zeros for tokens that take no
+ * part. */
+moe_status moe_balance_loss_backward(const float* logits, const uint8_t* mask,
+                                     const int32_t* seq_offsets, const int32_t* counts,
+                                     const int32_t* tokens, int T, int E, int k, int S, float coef,
+                                     const float* grad_loss, float* dlogits, void* stream);
+
 /* Layout conversion of fc1 from the Hugging Face chunked layout ("Weight layout":
  * [E, 2*inter, H], the first inter rows gate, the next inter rows up) to the
  * interleaved layout of swiglu_fusion = 1:  dst[e, 2j+s, :] = src[e, s*I + j, :].
@@ -271,7 +374,7 @@ const char* moe_status_string(moe_status s);
 
 /* ------------------------------------------------------------------------ profiling */
 
-/* Stage timing: when `events` is not NULL, moe_forward records the n_events (must
+/* Stage timing: when `events` is not NULL, moe_forward (and moe_forward_w8a8) records the n_events (must
  * be 6) cudaEvent_t handles on its stream: before routing, after routing, after the
  * permutation, after fc1 + SwiGLU, after fc2, after the combine.  NULL turns the
  * recording off.  The handles stay owned by the caller.  Process-wide setting. */

@@ -39,6 +39,18 @@ SIGNATURES = {
                             _i, _i, MoeSwiglu, _i, _vp, _vp, _sz, _vp]),
     "moe_expert_ffn_q8": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, MoeSwiglu,
                                _i, _vp, _vp, _sz, _vp]),
+    "moe_quantize_rows": (_i, [_vp, _i, _i, _i, _vp, _vp, _vp]),
+    "moe_matmul_q8": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _vp, _vp, _vp]),
+    "moe_expert_ffn_w8a8_workspace_size": (_sz, [_i, _i, _i, _i]),
+    "moe_expert_ffn_w8a8": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, MoeSwiglu,
+                                 _i, _vp, _vp, _sz, _vp]),
+    "moe_w8a8_workspace_size": (_sz, [_i, _i, _i, _i, _i]),
+    "moe_forward_w8a8": (_i, [_vp, _vp, _f, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i,
+                              _i, _i, MoeSwiglu, _i, _vp, _vp, _sz, _vp]),
+    "moe_balance_loss_workspace_size": (_sz, [_i, _i, _i]),
+    "moe_balance_loss": (_i, [_vp, _vp, _vp, _vp, _i, _i, _i, _i, _f, _vp, _vp, _vp, _vp, _vp, _vp,
+                              _sz, _vp]),
+    "moe_balance_loss_backward": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _f, _vp, _vp, _vp]),
     "convert_chunked_to_interleaved": (_i, [_vp, _vp, _i, _i, _i, _i, _vp]),
     "moe_get_error": (_i, [_vp, _vp, ctypes.POINTER(ctypes.c_int32)]),
     "moe_status_string": (ctypes.c_char_p, [_i]),

@@ -117,6 +117,64 @@ PermLayout perm_layout(int T, int E) {
     return L;
 }
 
+// Sizes of the int8 x int8 products: whole 16-byte K rows (TMA strides), 32 output
+// channels to a block; K bounded so that the int32 sums cannot overflow.
+constexpr int kQ8MaxK = 65536;
+constexpr int kMaxSequences = 65535;   // of the balance loss: one block each
+bool valid_q8_k(int K) { return K > 0 && K % 16 == 0 && K <= kQ8MaxK; }
+bool valid_q8_n(int N) { return N > 0 && N % 32 == 0; }
+bool valid_w8a8_ffn(int H, int I) {
+    return H > 0 && I > 0 && H % 32 == 0 && I % 32 == 0 && H <= kQ8MaxK && I <= kQ8MaxK;
+}
+
+// Workspace of the int8 expert FFN: error word, the int8 rows and scales of x_perm, the
+// float32 activations, their int8 rows and scales.
+struct W8a8Layout {
+    size_t err, xq, xs, act, aq, as, total;
+};
+
+W8a8Layout w8a8_layout(int rows, int H, int I) {
+    const size_t r = static_cast<size_t>(rows);
+    Carver c;
+    W8a8Layout L;
+    L.err = c.take(kAlign);
+    L.xq = c.take(r * H);
+    L.xs = c.take(r * 4);
+    L.act = c.take(r * I * 4);
+    L.aq = c.take(r * I);
+    L.as = c.take(r * 4);
+    L.total = c.off;
+    return L;
+}
+
+// Workspace of the layer with int8 experts: the routing's blocks (header and tile counts
+// first, cleared by one launch), the permuted rows, the FFN's workspace, its output.
+struct W8a8FwdLayout {
+    size_t tile_counts, logits, idx, w, near, counts, offsets, perm_src, perm_dst, x_perm, y, xn, ffn, total;
+};
+
+W8a8FwdLayout w8a8_fwd_layout(int T, int H, int E, int k, int I) {
+    const size_t rows = static_cast<size_t>(T) * k, t = static_cast<size_t>(T);
+    Carver c;
+    c.take(kAlign);   // [0] error word
+    W8a8FwdLayout L;
+    L.tile_counts = c.take(static_cast<size_t>(num_token_tiles(T)) * E * 4);
+    L.logits = c.take(t * E * 4);
+    L.idx = c.take(rows * 4);
+    L.w = c.take(rows * 4);
+    L.near = c.take(t * 4);
+    L.counts = c.take(static_cast<size_t>(E) * 4);
+    L.offsets = c.take(static_cast<size_t>(E + 1) * 4);
+    L.perm_src = c.take(rows * 4);
+    L.perm_dst = c.take(rows * 4);
+    L.x_perm = c.take(rows * H * 2);
+    L.y = c.take(rows * H * 2);
+    L.xn = c.take(t * H * 2);   // the normalised input (pre-FFN norm)
+    L.ffn = c.take(w8a8_layout(static_cast<int>(rows), H, I).total);
+    L.total = c.off;
+    return L;
+}
+
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 bool valid_dtype(moe_dtype dt) { return dt == MOE_F32 || dt == MOE_BF16; }
@@ -202,6 +260,71 @@ cudaError_t gather_rows(const void* hidden, const int32_t* perm_src, const int32
     return launch_gather(hidden, perm_src, offsets, E, T, T * k, H, es, x_perm, s);
 }
 
+// What the staged routing writes (workspace blocks of the layer).
+struct RouteBufs {
+    float* logits;
+    int32_t* idx;
+    float* w;
+    int32_t *near, *counts, *offsets, *perm_src, *perm_dst, *tile_counts, *err;
+    int32_t* zero_words;   // cleared on the way by the small route (or nullptr)
+    int n_zero;
+};
+
+// Routing, counts, offsets and the stable permutation with the staged kernels of `path`
+// (the small route, the tensor-core router or the SIMT one).
+moe_status staged_routing(int path, const void* hidden, const void* router_w, const float* router_bias,
+                          int T, int H, int E, int k, int normalize, bool bf16, const RouteBufs& rb,
+                          cudaStream_t s) {
+    if (path & kPathSmallRoute) {
+        // logits on many CTAs (which also clear the header), then one CTA for top-k,
+        // bincount, scan and the stable permutation
+        MOE_CUDA(launch_router_logits_split(hidden, router_w, T, H, E, bf16, rb.logits, rb.err, s));
+        RouteSmallArgs a;
+        a.logits = rb.logits;
+        a.bias = router_bias;
+        a.T = T;
+        a.E = E;
+        a.k = k;
+        a.normalize = normalize ? 1 : 0;
+        a.topk_idx = rb.idx;
+        a.topk_w = rb.w;
+        a.near_tie = rb.near;
+        a.counts = rb.counts;
+        a.offsets = rb.offsets;
+        a.perm_src = rb.perm_src;
+        a.perm_dst = rb.perm_dst;
+        a.zero_words = rb.zero_words;
+        a.n_zero = rb.n_zero;
+        MOE_CUDA(launch_route_small(a, s));
+        record(1, s);
+        return MOE_OK;
+    }
+    if (path & kPathTcRouter) {
+        // logits on the tensor cores, routing and per-tile bincount in the epilogue
+        MOE_CUDA(launch_route_tc(hidden, router_w, router_bias, T, H, E, k, normalize, rb.idx, rb.w,
+                                 rb.near, nullptr, rb.tile_counts, rb.err, s));
+    } else {
+        MOE_CUDA(launch_router_logits_simt(hidden, router_w, T, H, E, bf16, rb.logits, s));
+        TopkHistArgs a;
+        a.logits = rb.logits;
+        a.bias = router_bias;
+        a.T = T;
+        a.E = E;
+        a.k = k;
+        a.normalize = normalize ? 1 : 0;
+        a.topk_idx = rb.idx;
+        a.topk_w = rb.w;
+        a.near_tie = rb.near;
+        a.tile_counts = rb.tile_counts;
+        a.err = rb.err;
+        MOE_CUDA(launch_topk_hist(a, s));
+    }
+    record(1, s);
+    MOE_CUDA(launch_scatter(rb.idx, rb.tile_counts, T, E, k, rb.counts, rb.offsets, rb.perm_src,
+                            rb.perm_dst, rb.err, s));
+    return MOE_OK;
+}
+
 }  // namespace
 }  // namespace moe
 
@@ -209,7 +332,7 @@ using namespace moe;
 
 extern "C" {
 
-int moe_version(void) { return 220; }
+int moe_version(void) { return 230; }
 
 void moe_debug_arm_route_barrier_timeout(void) { arm_route_timeout_test(); }
 
@@ -505,56 +628,14 @@ static moe_status forward_impl(const void* hidden, const void* norm_weight, floa
         record(5, s);
         return MOE_OK;
     }
-    if (path & kPathSmallRoute) {
-        // logits on many CTAs (which also clear the header), then one CTA for top-k,
-        // bincount, scan and the stable permutation
-        MOE_CUDA(launch_router_logits_split(hidden, router_w, T, H, E, bf16, logits, err, s));
-        RouteSmallArgs a;
-        a.logits = logits;
-        a.bias = router_bias;
-        a.T = T;
-        a.E = E;
-        a.k = k;
-        a.normalize = normalize ? 1 : 0;
-        a.topk_idx = idx;
-        a.topk_w = w;
-        a.near_tie = near;
-        a.counts = counts;
-        a.offsets = offsets;
-        a.perm_src = perm_src;
-        a.perm_dst = perm_dst;
-        if (path & kPathDecodeFfn) {
-            a.zero_words = ctr;
-            a.n_zero = decode_ffn_counters(rows, E);
-        }
-        MOE_CUDA(launch_route_small(a, s));
-        record(1, s);
-    } else {
-        int32_t* tile_counts = reinterpret_cast<int32_t*>(ws + L.tile_counts);
-        if (path & kPathTcRouter) {
-            // logits on the tensor cores, routing and per-tile bincount in the epilogue
-            MOE_CUDA(launch_route_tc(hidden, router_w, router_bias, T, H, E, k, normalize, idx, w,
-                                     near, nullptr, tile_counts, err, s));
-        } else {
-            MOE_CUDA(launch_router_logits_simt(hidden, router_w, T, H, E, bf16, logits, s));
-            TopkHistArgs a;
-            a.logits = logits;
-            a.bias = router_bias;
-            a.T = T;
-            a.E = E;
-            a.k = k;
-            a.normalize = normalize ? 1 : 0;
-            a.topk_idx = idx;
-            a.topk_w = w;
-            a.near_tie = near;
-            a.tile_counts = tile_counts;
-            a.err = err;
-            MOE_CUDA(launch_topk_hist(a, s));
-        }
-        record(1, s);
-        MOE_CUDA(launch_scatter(idx, tile_counts, T, E, k, counts, offsets, perm_src, perm_dst,
-                                err, s));
+    RouteBufs rb{logits, idx, w, near, counts, offsets, perm_src, perm_dst,
+                 reinterpret_cast<int32_t*>(ws + L.tile_counts), err, nullptr, 0};
+    if (path & kPathDecodeFfn) {
+        rb.zero_words = ctr;
+        rb.n_zero = decode_ffn_counters(rows, E);
     }
+    const moe_status routed = staged_routing(path, hidden, router_w, router_bias, T, H, E, k, normalize, bf16, rb, s);
+    if (routed != MOE_OK) return routed;
     if (path & kPathDecodeFfn) {
         // fc1 + SwiGLU and fc2 in one launch.  With at most 4 rows per expert on
         // average, fc1 gathers its token rows straight from hidden (tile::gather4, four
@@ -646,6 +727,251 @@ moe_status moe_expert_ffn_q8(const void* x_perm, const int32_t* offsets, const i
     MOE_CUDA(cudaMemsetAsync(ctr, 0, static_cast<size_t>(decode_ffn_counters(rows, E)) * 4, s));
     MOE_CUDA(launch_ffn_decode(x_perm, nullptr, rows, offsets, fc1_q, fc2_q, rows, H, E, I, act_buf,
                                y_perm, ctr, err, nullptr, nullptr, 0, nullptr, s, ep));
+    return MOE_OK;
+}
+
+moe_status moe_quantize_rows(const void* x, int rows, int K, moe_dtype dt, int8_t* q, float* scale,
+                             void* stream) {
+    if (rows < 0 || K <= 0 || K % 8 || !valid_dtype(dt)) return MOE_ERR_INVALID_ARG;
+    if (rows == 0) return MOE_OK;
+    if (!x || !q || !scale || !aligned(x, 16) || !aligned(q, 16) || !aligned(scale, 4))
+        return MOE_ERR_INVALID_ARG;
+    MOE_CUDA(launch_quantize_rows(x, rows, K, dt == MOE_BF16, q, scale, static_cast<cudaStream_t>(stream)));
+    return MOE_OK;
+}
+
+moe_status moe_matmul_q8(const int8_t* a_q, const float* a_scale, const int8_t* w_q,
+                         const float* w_scale, const void* bias, const int32_t* offsets, int rows,
+                         int K, int E, int N, moe_dtype out_dt, void* out, int32_t* err_word,
+                         void* stream) {
+    if (rows < 0 || E <= 0 || E > kMaxExperts || !valid_q8_k(K) || !valid_q8_n(N) || !valid_dtype(out_dt) ||
+        (!offsets && E != 1))
+        return MOE_ERR_INVALID_ARG;
+    if (rows == 0) return MOE_OK;
+    if (!a_q || !a_scale || !w_q || !w_scale || !out) return MOE_ERR_INVALID_ARG;
+    if (!aligned(a_q, 16) || !aligned(w_q, 16) || !aligned(out, 16) || !aligned(a_scale, 4) ||
+        !aligned(w_scale, 4) || (bias && !aligned(bias, elem_size(out_dt))) ||
+        (offsets && !aligned(offsets, 4)) || (err_word && !aligned(err_word, 4)))
+        return MOE_ERR_INVALID_ARG;
+    Q8GemmArgs g;
+    g.a_q = a_q;
+    g.a_scale = a_scale;
+    g.w_q = w_q;
+    g.w_scale = w_scale;
+    g.bias = bias;
+    g.offsets = offsets;
+    g.rows = rows;
+    g.K = K;
+    g.E = E;
+    g.N = N;
+    g.out_bf16 = out_dt == MOE_BF16;
+    g.out = out;
+    g.err = err_word;
+    MOE_CUDA(launch_q8_gemm(g, static_cast<cudaStream_t>(stream)));
+    return MOE_OK;
+}
+
+size_t moe_expert_ffn_w8a8_workspace_size(int rows, int H, int E, int I) {
+    if (rows < 0 || E <= 0 || E > kMaxExperts || !valid_w8a8_ffn(H, I)) return 0;
+    return w8a8_layout(rows, H, I).total;
+}
+
+// The int8 expert FFN of valid arguments; err is cleared by the caller.
+static moe_status w8a8_ffn(const void* x_perm, const int32_t* offsets, const int8_t* fc1_q,
+                           const float* fc1_scale, const int8_t* fc2_q, const float* fc2_scale, int rows,
+                           int H, int E, int I, const FfnAttrs& ep, void* y_perm, char* ws,
+                           const W8a8Layout& L, int32_t* err, cudaStream_t s, cudaEvent_t mid) {
+    int8_t* xq = reinterpret_cast<int8_t*>(ws + L.xq);
+    float* xs = reinterpret_cast<float*>(ws + L.xs);
+    float* act = reinterpret_cast<float*>(ws + L.act);
+    int8_t* aq = reinterpret_cast<int8_t*>(ws + L.aq);
+    float* as = reinterpret_cast<float*>(ws + L.as);
+    MOE_CUDA(launch_quantize_rows(x_perm, rows, H, true, xq, xs, s));
+    Q8GemmArgs g;
+    g.a_q = xq;
+    g.a_scale = xs;
+    g.w_q = fc1_q;
+    g.w_scale = fc1_scale;
+    g.bias = ep.fc1_bias;
+    g.offsets = offsets;
+    g.rows = rows;
+    g.K = H;
+    g.E = E;
+    g.N = 2 * I;
+    g.swiglu = true;
+    g.act = ep.act;
+    g.fc1_chunked = ep.fc1_chunked;
+    g.out = act;
+    g.err = err;
+    MOE_CUDA(launch_q8_gemm(g, s));
+    if (mid) record_event(mid, s);
+    MOE_CUDA(launch_quantize_rows(act, rows, I, false, aq, as, s));
+    g = Q8GemmArgs();
+    g.a_q = aq;
+    g.a_scale = as;
+    g.w_q = fc2_q;
+    g.w_scale = fc2_scale;
+    g.bias = ep.fc2_bias;
+    g.offsets = offsets;
+    g.rows = rows;
+    g.K = I;
+    g.E = E;
+    g.N = H;
+    g.out = y_perm;
+    g.err = err;
+    MOE_CUDA(launch_q8_gemm(g, s));
+    return MOE_OK;
+}
+
+moe_status moe_expert_ffn_w8a8(const void* x_perm, const int32_t* offsets, const int8_t* fc1_q,
+                               const float* fc1_scale, const int8_t* fc2_q, const float* fc2_scale,
+                               const void* fc1_bias, const void* fc2_bias, int rows, int H, int E,
+                               int I, moe_swiglu act, moe_fc1_layout fc1_layout, void* y_perm,
+                               void* workspace, size_t ws_bytes, void* stream) {
+    if (rows < 0 || E <= 0 || E > kMaxExperts || !valid_w8a8_ffn(H, I) || !valid_swiglu(act) ||
+        !valid_layout(fc1_layout))
+        return MOE_ERR_INVALID_ARG;
+    if (rows == 0) return MOE_OK;
+    if (!x_perm || !offsets || !fc1_q || !fc1_scale || !fc2_q || !fc2_scale || !y_perm || !workspace)
+        return MOE_ERR_INVALID_ARG;
+    if (!aligned(x_perm, 16) || !aligned(offsets, 4) || !aligned(fc1_q, 16) || !aligned(fc2_q, 16) ||
+        !aligned(fc1_scale, 4) || !aligned(fc2_scale, 4) || !aligned(y_perm, 16) ||
+        !aligned(workspace, kAlign) || (fc1_bias && !aligned(fc1_bias, 2)) ||
+        (fc2_bias && !aligned(fc2_bias, 2)))
+        return MOE_ERR_INVALID_ARG;
+    const W8a8Layout L = w8a8_layout(rows, H, I);
+    if (ws_bytes < L.total) return MOE_ERR_INVALID_ARG;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    char* ws = static_cast<char*>(workspace);
+    int32_t* err = reinterpret_cast<int32_t*>(ws + L.err);
+    MOE_CUDA(launch_clear(err, kAlign, s));
+    return w8a8_ffn(x_perm, offsets, fc1_q, fc1_scale, fc2_q, fc2_scale, rows, H, E, I,
+                    make_ffn_attrs(act, fc1_layout, fc1_bias, fc2_bias), y_perm, ws, L, err, s, nullptr);
+}
+
+size_t moe_w8a8_workspace_size(int T, int H, int E, int k, int I) {
+    if (!valid_sizes(T, H, E, k) || !valid_w8a8_ffn(H, I)) return 0;
+    return w8a8_fwd_layout(T, H, E, k, I).total;
+}
+
+moe_status moe_forward_w8a8(const void* hidden, const void* norm_weight, float norm_eps,
+                            const void* router_w, const float* router_bias, const int8_t* fc1_q,
+                            const float* fc1_scale, const int8_t* fc2_q, const float* fc2_scale,
+                            const void* fc1_bias, const void* fc2_bias, int T, int H, int E, int k,
+                            int I, int normalize, moe_swiglu act, moe_fc1_layout fc1_layout,
+                            void* out, void* workspace, size_t ws_bytes, void* stream) {
+    if (!valid_sizes(T, H, E, k) || !valid_w8a8_ffn(H, I) || !valid_swiglu(act) ||
+        !valid_layout(fc1_layout) || (norm_weight && !valid_eps(norm_eps)))
+        return MOE_ERR_INVALID_ARG;
+    if (T == 0) return MOE_OK;
+    if (!hidden || !router_w || !fc1_q || !fc1_scale || !fc2_q || !fc2_scale || !out || !workspace)
+        return MOE_ERR_INVALID_ARG;
+    if (!aligned(hidden, 16) || !aligned(router_w, 16) || !aligned(fc1_q, 16) || !aligned(fc2_q, 16) ||
+        !aligned(fc1_scale, 4) || !aligned(fc2_scale, 4) || !aligned(out, 16) ||
+        !aligned(workspace, kAlign) || (norm_weight && !aligned(norm_weight, 16)) ||
+        (router_bias && !aligned(router_bias, 4)) || (fc1_bias && !aligned(fc1_bias, 2)) ||
+        (fc2_bias && !aligned(fc2_bias, 2)))
+        return MOE_ERR_INVALID_ARG;
+    const W8a8FwdLayout L = w8a8_fwd_layout(T, H, E, k, I);
+    if (ws_bytes < L.total) return MOE_ERR_INVALID_ARG;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    char* ws = static_cast<char*>(workspace);
+    const int rows = T * k;
+    record(0, s);
+    // the routing reads the bf16 input; its error word is the workspace's first word
+    const size_t clear_end = L.logits;
+    if (norm_weight) {
+        MOE_CUDA(launch_rmsnorm(hidden, norm_weight, T, H, norm_eps, true, ws + L.xn, ws, clear_end, s));
+        hidden = ws + L.xn;
+    } else {
+        MOE_CUDA(launch_clear(ws, clear_end, s));
+    }
+    int path = 0;
+    if (T > kRouteSmallTcT && tc_route_supported(H, E, k)) path = kPathTcRouter;
+    else if (T <= kRouteSmallMaxT && k <= kRouteSmallMaxK) path = kPathSmallRoute;
+    auto i32 = [&](size_t off) { return reinterpret_cast<int32_t*>(ws + off); };
+    const RouteBufs rb{reinterpret_cast<float*>(ws + L.logits), i32(L.idx),
+                       reinterpret_cast<float*>(ws + L.w), i32(L.near), i32(L.counts), i32(L.offsets),
+                       i32(L.perm_src), i32(L.perm_dst), i32(L.tile_counts), i32(0), nullptr, 0};
+    moe_status st = staged_routing(path, hidden, router_w, router_bias, T, H, E, k, normalize, true, rb, s);
+    if (st != MOE_OK) return st;
+    MOE_CUDA(gather_rows(hidden, rb.perm_src, rb.perm_dst, rb.offsets, T, E, k, H, MOE_BF16, ws + L.x_perm, s));
+    record(2, s);
+    st = w8a8_ffn(ws + L.x_perm, rb.offsets, fc1_q, fc1_scale, fc2_q, fc2_scale, rows, H, E, I,
+                  make_ffn_attrs(act, fc1_layout, fc1_bias, fc2_bias), ws + L.y, ws + L.ffn,
+                  w8a8_layout(rows, H, I), i32(0), s, g_events_on ? g_events[3] : nullptr);
+    if (st != MOE_OK) return st;
+    record(4, s);
+    MOE_CUDA(launch_combine(ws + L.y, rb.perm_dst, rb.w, T, H, k, true, out, s));
+    record(5, s);
+    return MOE_OK;
+}
+
+size_t moe_balance_loss_workspace_size(int T, int E, int S) {
+    if (T < 0 || E <= 0 || E > kMaxExperts || S < 1 || S > kMaxSequences) return 0;
+    return balance_workspace_bytes(T, E, S);
+}
+
+moe_status moe_balance_loss(const float* logits, const int32_t* topk_idx, const uint8_t* mask,
+                            const int32_t* seq_offsets, int T, int E, int k, int S, float coef,
+                            float* loss, int32_t* counts, float* probs, int32_t* tokens,
+                            int32_t* err_word, void* workspace, size_t ws_bytes, void* stream) {
+    if (T < 0 || E <= 0 || E > kMaxExperts || k < 1 || k > E || static_cast<long long>(T) * k > (1LL << 30) ||
+        S < 1 || S > kMaxSequences || (!seq_offsets && S != 1) || !isfinite(coef))
+        return MOE_ERR_INVALID_ARG;
+    if ((T > 0 && (!logits || !topk_idx)) || !loss || !counts || !probs || !tokens || !workspace)
+        return MOE_ERR_INVALID_ARG;
+    if (!aligned(logits, 16) || !aligned(topk_idx, 4) || (seq_offsets && !aligned(seq_offsets, 4)) ||
+        !aligned(loss, 4) || !aligned(counts, 4) || !aligned(probs, 4) || !aligned(tokens, 4) ||
+        (err_word && !aligned(err_word, 4)) || !aligned(workspace, kAlign))
+        return MOE_ERR_INVALID_ARG;
+    if (ws_bytes < balance_workspace_bytes(T, E, S)) return MOE_ERR_INVALID_ARG;
+    BalanceArgs a;
+    a.logits = logits;
+    a.topk_idx = topk_idx;
+    a.mask = mask;
+    a.seq_offsets = seq_offsets;
+    a.T = T;
+    a.E = E;
+    a.k = k;
+    a.S = S;
+    a.coef = coef;
+    a.loss = loss;
+    a.counts = counts;
+    a.probs = probs;
+    a.tokens = tokens;
+    a.err = err_word;
+    a.workspace = workspace;
+    MOE_CUDA(launch_balance_loss(a, static_cast<cudaStream_t>(stream)));
+    return MOE_OK;
+}
+
+moe_status moe_balance_loss_backward(const float* logits, const uint8_t* mask,
+                                     const int32_t* seq_offsets, const int32_t* counts,
+                                     const int32_t* tokens, int T, int E, int k, int S, float coef,
+                                     const float* grad_loss, float* dlogits, void* stream) {
+    if (T < 0 || E <= 0 || E > kMaxExperts || k < 1 || k > E || static_cast<long long>(T) * k > (1LL << 30) ||
+        S < 1 || S > kMaxSequences || (!seq_offsets && S != 1) || !isfinite(coef))
+        return MOE_ERR_INVALID_ARG;
+    if (T == 0) return MOE_OK;
+    if (!logits || !counts || !tokens || !dlogits) return MOE_ERR_INVALID_ARG;
+    if (!aligned(logits, 16) || (seq_offsets && !aligned(seq_offsets, 4)) || !aligned(counts, 4) ||
+        !aligned(tokens, 4) || (grad_loss && !aligned(grad_loss, 4)) || !aligned(dlogits, 16))
+        return MOE_ERR_INVALID_ARG;
+    BalanceGradArgs a;
+    a.logits = logits;
+    a.mask = mask;
+    a.seq_offsets = seq_offsets;
+    a.counts = counts;
+    a.tokens = tokens;
+    a.T = T;
+    a.E = E;
+    a.k = k;
+    a.S = S;
+    a.coef = coef;
+    a.grad_loss = grad_loss;
+    a.dlogits = dlogits;
+    MOE_CUDA(launch_balance_grad(a, static_cast<cudaStream_t>(stream)));
     return MOE_OK;
 }
 

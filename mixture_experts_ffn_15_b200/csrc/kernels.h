@@ -185,6 +185,60 @@ cudaError_t launch_ffn_pair(const void* x_perm, const int32_t* offsets, const vo
                             const void* fc2, int rows, int H, int E, int I, void* act, void* y,
                             int32_t* err, cudaStream_t s, cudaEvent_t mid, const FfnAttrs& ep);
 
+// ---------------------------------------------------------------- quantize.cu
+// q [rows, K] int8 and scale [rows] of x [rows, K] (bf16 or float32; K a multiple of 8).
+cudaError_t launch_quantize_rows(const void* x, int rows, int K, bool bf16, int8_t* q, float* scale,
+                                 cudaStream_t s);
+
+// ---------------------------------------------------------------- gemm_q8.cu
+// One grouped product of int8 rows and int8 weights (K a multiple of 16, N of 32).
+struct Q8GemmArgs {
+    const int8_t* a_q = nullptr;       // [rows, K]
+    const float* a_scale = nullptr;    // [rows]
+    const int8_t* w_q = nullptr;       // [E, N, K]
+    const float* w_scale = nullptr;    // [E, N]
+    const void* bias = nullptr;        // [E, N] (bf16, or float32 with a float32 output) or nullptr
+    const int32_t* offsets = nullptr;  // [E + 1] device, or nullptr: one expert owns every row
+    int rows = 0, K = 0, E = 1, N = 0;
+    bool out_bf16 = true;              // plain product: out [rows, N] bf16 or float32
+    bool swiglu = false;               // fc1: out [rows, N / 2] float32, activations
+    SwigluAttr act{1.0f, 0.0f, INFINITY, 1};
+    bool fc1_chunked = false;          // swiglu: weight rows, scales and bias in the chunked layout
+    void* out = nullptr;
+    int32_t* err = nullptr;            // device error word or nullptr
+};
+cudaError_t launch_q8_gemm(const Q8GemmArgs& a, cudaStream_t s);
+
+// ---------------------------------------------------------------- balance.cu
+size_t balance_workspace_bytes(int T, int E, int S);
+struct BalanceArgs {
+    const float* logits = nullptr;         // [T, E]
+    const int32_t* topk_idx = nullptr;     // [T, k]
+    const uint8_t* mask = nullptr;         // [T] or nullptr
+    const int32_t* seq_offsets = nullptr;  // [S + 1] or nullptr (S = 1)
+    int T = 0, E = 0, k = 0, S = 1;
+    float coef = 1.f;
+    float* loss = nullptr;                 // [1]
+    int32_t* counts = nullptr;             // [S, E]
+    float* probs = nullptr;                // [S, E]
+    int32_t* tokens = nullptr;             // [S]
+    int32_t* err = nullptr;
+    void* workspace = nullptr;
+};
+cudaError_t launch_balance_loss(const BalanceArgs& a, cudaStream_t s);
+struct BalanceGradArgs {
+    const float* logits = nullptr;
+    const uint8_t* mask = nullptr;
+    const int32_t* seq_offsets = nullptr;
+    const int32_t* counts = nullptr;
+    const int32_t* tokens = nullptr;
+    int T = 0, E = 0, k = 0, S = 1;
+    float coef = 1.f;
+    const float* grad_loss = nullptr;      // [1] or nullptr (1)
+    float* dlogits = nullptr;              // [T, E]
+};
+cudaError_t launch_balance_grad(const BalanceGradArgs& a, cudaStream_t s);
+
 // Decode FFN: fc1 + SwiGLU and fc2 in one persistent launch (weight rows on M).
 bool decode_ffn_supported(int rows, int E, int H, int I);
 int decode_ffn_counters(int rows, int E);   // int32 counters it needs, zero on entry

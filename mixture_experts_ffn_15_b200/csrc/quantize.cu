@@ -1,0 +1,139 @@
+// int8 rows with one float32 scale each (symmetric, per token):
+//   amax_r = max_k |x[r, k]|,  scale[r] = amax_r / 127 (float32 division),
+//   q[r, k] = 127 x[r, k] / amax_r rounded to the nearest whole number, ties to even.
+// A row of zeros has scale 0 and q = 0; a row that holds an infinity or a NaN has scale
+// NaN and q = 0, so that whatever is multiplied with it comes out NaN, as it would in
+// floating point.
+//
+// The whole number is the exact one, for every float32 and bf16 input: v = x (127 / amax)
+// in float32 is within 127 * 2^-23 = 1.6e-5 of the exact quotient, so its rounding can be
+// wrong only where v lies within that distance of a half; values within 1e-4 of a half
+// (one in 5000) take the quotient in float64 instead.  There 127 x is exact, and the
+// quotient of two 24-bit significands is either exactly a half or at least 2^-32 of its
+// value away from it, far more than float64's rounding.
+//
+// One pass over the row: a row's threads keep their vectors of 8 elements in registers
+// between the maximum and the rounding (rows longer than kRegVec vectors a thread read the
+// rest again, from L2).  Bound by HBM: rows K (2 or 4) bytes read, rows (K + 4) written.
+#include "common.cuh"
+#include "kernels.h"
+#include "quantize.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kQThreads = 256;
+constexpr int kRegVec = 4;
+
+template <bool BF16>
+struct Vec8 {
+    uint4 a, b;   // bf16: a only
+    __device__ __forceinline__ void load(const void* x, size_t row, int nvec, int v) {
+        if constexpr (BF16) {
+            a = __ldg(reinterpret_cast<const uint4*>(x) + row * nvec + v);
+        } else {
+            const uint4* p = reinterpret_cast<const uint4*>(x) + (row * nvec + v) * 2;
+            a = __ldg(p);
+            b = __ldg(p + 1);
+        }
+    }
+    __device__ __forceinline__ void get(float* f) const {
+        if constexpr (BF16) {
+            unpack_bf16x8(a, f);
+        } else {
+            const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+            for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(w[i]);
+        }
+    }
+    // bits of the largest |element|, as float32 (a NaN is larger than an infinity)
+    __device__ __forceinline__ uint32_t amax() const {
+        float f[8];
+        get(f);
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(f[i]) & 0x7fffffffu);
+        return m;
+    }
+};
+
+// TPR threads (a power of two, 32 .. 256) share a row.
+template <bool BF16, int TPR>
+__global__ void __launch_bounds__(kQThreads)
+quantize_rows_kernel(const void* __restrict__ x, int rows, int K, int8_t* __restrict__ q,
+                     float* __restrict__ scale) {
+    constexpr int kRows = kQThreads / TPR;   // rows of a block
+    __shared__ uint32_t s_max[kQThreads / 32];
+    pdl_wait();
+    pdl_trigger();
+    const int nvec = K / 8;
+    const int t = threadIdx.x % TPR;
+    const long long row = static_cast<long long>(blockIdx.x) * kRows + threadIdx.x / TPR;
+    const bool live = row < rows;
+    Vec8<BF16> r[kRegVec];
+    uint32_t m = 0;
+    if (live) {
+#pragma unroll
+        for (int j = 0; j < kRegVec; ++j)
+            if (t + j * TPR < nvec) r[j].load(x, row, nvec, t + j * TPR);
+#pragma unroll
+        for (int j = 0; j < kRegVec; ++j)
+            if (t + j * TPR < nvec) m = max(m, r[j].amax());
+        for (int v = t + kRegVec * TPR; v < nvec; v += TPR) {
+            Vec8<BF16> w;
+            w.load(x, row, nvec, v);
+            m = max(m, w.amax());
+        }
+    }
+    m = __reduce_max_sync(0xffffffffu, m);
+    if constexpr (TPR > 32) {
+        if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = m;
+        __syncthreads();
+        const int w0 = (threadIdx.x / TPR) * (TPR / 32);
+#pragma unroll
+        for (int i = 0; i < TPR / 32; ++i) m = max(m, s_max[w0 + i]);
+    }
+    if (!live) return;
+    const RowQuant rq = row_quant(m);
+    if (t == 0) scale[row] = rq.scale;
+    uint2* out = reinterpret_cast<uint2*>(q) + row * nvec;
+    float f[8];
+#pragma unroll
+    for (int j = 0; j < kRegVec; ++j)
+        if (t + j * TPR < nvec) {
+            r[j].get(f);
+            out[t + j * TPR] = quantize8(f, rq);
+        }
+    for (int v = t + kRegVec * TPR; v < nvec; v += TPR) {
+        Vec8<BF16> w;
+        w.load(x, row, nvec, v);
+        w.get(f);
+        out[v] = quantize8(f, rq);
+    }
+}
+
+template <bool BF16>
+cudaError_t launch(const void* x, int rows, int K, int8_t* q, float* scale, cudaStream_t s) {
+    const int nvec = K / 8;
+    // threads a row: what holds it in registers
+    int tpr = 32;
+    while (tpr < kQThreads && tpr * kRegVec < nvec) tpr *= 2;
+    const int per = kQThreads / tpr;
+    const dim3 grid(static_cast<unsigned>((rows + per - 1) / per)), block(kQThreads);
+    switch (tpr) {
+        case 32: return launch_k(quantize_rows_kernel<BF16, 32>, grid, block, 0, s, x, rows, K, q, scale);
+        case 64: return launch_k(quantize_rows_kernel<BF16, 64>, grid, block, 0, s, x, rows, K, q, scale);
+        case 128: return launch_k(quantize_rows_kernel<BF16, 128>, grid, block, 0, s, x, rows, K, q, scale);
+        default: return launch_k(quantize_rows_kernel<BF16, 256>, grid, block, 0, s, x, rows, K, q, scale);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_quantize_rows(const void* x, int rows, int K, bool bf16, int8_t* q, float* scale,
+                                 cudaStream_t s) {
+    if (rows <= 0) return cudaSuccess;
+    return bf16 ? launch<true>(x, rows, K, q, scale, s) : launch<false>(x, rows, K, q, scale, s);
+}
+
+}  // namespace moe

@@ -5,6 +5,7 @@ the CUDA kernels of libmoe_b200.so.  These functions check dtypes, devices, shap
 and contiguity, allocate outputs and workspaces with torch when the caller does
 not pass them, and raise MoEError on any non-OK status.
 """
+import contextlib
 import ctypes
 
 import torch
@@ -182,6 +183,243 @@ def expert_ffn_q8(x_perm, offsets, fc1_q, fc1_scale, fc2_q, fc2_scale, y_perm=No
                                   _ptr(ws), ws.numel(), _stream(stream))
     check(st, "moe_expert_ffn_q8")
     return y_perm
+
+
+def _same_device(t, *others):
+    for o in others:
+        if o is not None and o.device != t.device:
+            raise ValueError(f"every tensor must be on {t.device}, got one on {o.device}")
+
+
+_HERE = contextlib.nullcontext()
+
+
+def _on(t, stream):
+    """(stream, context) of a call: the caller's stream, or the current one of t's device.
+    What is allocated inside the context belongs to that stream; the context is empty where
+    the stream is the current one already."""
+    if stream is None:
+        s = torch.cuda.current_stream(t.device)
+        return s, (_HERE if t.device.index == torch.cuda.current_device() else torch.cuda.stream(s))
+    if stream.device != t.device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors are on {t.device}")
+    return stream, torch.cuda.stream(stream)
+
+
+def quantize_rows(x, q=None, scale=None, stream=None):
+    """x [rows, K] (bf16 or float32) -> (q [rows, K] int8, scale [rows] float32): per row
+    scale = max|x| / 127 and q = 127 x / max|x| to the nearest whole number, ties to even
+    (exact).  A zero row gives scale 0 and q 0; one with an infinity or a NaN scale NaN
+    and q 0."""
+    _need(x, "x")
+    rows, K = x.shape
+    s, here = _on(x, stream)
+    with here:
+        if q is None:
+            q = torch.empty((rows, K), dtype=torch.int8, device=x.device)
+        if scale is None:
+            scale = torch.empty((rows,), dtype=torch.float32, device=x.device)
+        _need(q, "q", torch.int8, (rows, K))
+        _need(scale, "scale", torch.float32, (rows,))
+        _same_device(x, q, scale)
+        check(_lib().moe_quantize_rows(_ptr(x), rows, K, _dtcode(x), _ptr(q), _ptr(scale),
+                                       _stream(s)), "moe_quantize_rows")
+    return q, scale
+
+
+def matmul_q8(a_q, a_scale, w_q, w_scale, offsets=None, bias=None, out=None,
+              out_dtype=torch.bfloat16, err_word=None, stream=None):
+    """out[r, n] = (sum_k a_q[r, k] w_q[e, n, k]) a_scale[r] w_scale[e, n] + bias[e, n]:
+    int8 rows (quantize_rows) times int8 weights, the sum exact.  Dense (w_q [N, K],
+    w_scale and bias [N]) or, with offsets [E+1], grouped: rows offsets[e] ..
+    offsets[e+1]-1 meet w_q[e] of w_q [E, N, K] (w_scale and bias [E, N]); rows at or
+    beyond offsets[E] are not written (zeros when out is not given).  out, and bias, are
+    bf16 or float32 (out_dtype, or out's own)."""
+    _need(a_q, "a_q", torch.int8)
+    rows, K = a_q.shape
+    _need(a_scale, "a_scale", torch.float32, (rows,))
+    grouped = offsets is not None
+    if w_q.dim() != (3 if grouped else 2):
+        raise ValueError("w_q must be [E, N, K] with offsets, [N, K] without")
+    E, N = (w_q.shape[0], w_q.shape[1]) if grouped else (1, w_q.shape[0])
+    lead = (E, N) if grouped else (N,)
+    _need(w_q, "w_q", torch.int8, lead + (K,))
+    _need(w_scale, "w_scale", torch.float32, lead)
+    if grouped:
+        _need(offsets, "offsets", torch.int32, (E + 1,))
+    if err_word is not None:
+        _need(err_word, "err_word", torch.int32)
+    s, here = _on(a_q, stream)
+    with here:
+        if out is None:
+            out = (torch.zeros if grouped else torch.empty)((rows, N), dtype=out_dtype, device=a_q.device)
+        dt = _dtcode(out)
+        _need(out, "out", None, (rows, N))
+        if bias is not None:
+            _need(bias, "bias", out.dtype, lead)
+        _same_device(a_q, a_scale, w_q, w_scale, offsets, bias, out, err_word)
+        check(_lib().moe_matmul_q8(_ptr(a_q), _ptr(a_scale), _ptr(w_q), _ptr(w_scale), _ptr(bias),
+                                   _ptr(offsets), rows, K, E, N, dt, _ptr(out), _ptr(err_word),
+                                   _stream(s)), "moe_matmul_q8")
+    return out
+
+
+def expert_ffn_w8a8_workspace_size(rows, H, E, I):
+    """Bytes of workspace expert_ffn_w8a8 needs (0 for sizes it rejects)."""
+    return _lib().moe_expert_ffn_w8a8_workspace_size(rows, H, E, I)
+
+
+def expert_ffn_w8a8(x_perm, offsets, fc1_q, fc1_scale, fc2_q, fc2_scale, y_perm=None,
+                    workspace=None, stream=None, swiglu=(1.0, 0.0, float("inf")), fc1_bias=None,
+                    fc2_bias=None, fc1_layout="interleaved"):
+    """expert_ffn with int8 weights and int8 activations (quantize_rows before either
+    product), for any number of rows per expert; weights and scales as in forward_q8.
+    Rows at or beyond offsets[E] are not written (zeros when y_perm is not given).  The
+    workspace's first word is the call's error word (get_error)."""
+    _need(x_perm, "x_perm", torch.bfloat16)
+    rows, H = x_perm.shape
+    E, two_i, _ = fc1_q.shape
+    I = two_i // 2
+    _need(offsets, "offsets", torch.int32, (E + 1,))
+    _q8(fc1_q, fc1_scale, "fc1", (E, 2 * I, H))
+    _q8(fc2_q, fc2_scale, "fc2", (E, H, I))
+    _biases(fc1_bias, fc2_bias, torch.bfloat16, E, I, H)
+    s, here = _on(x_perm, stream)
+    with here:
+        if y_perm is None:
+            y_perm = torch.zeros_like(x_perm)
+        _need(y_perm, "y_perm", torch.bfloat16, (rows, H))
+        if workspace is None:
+            workspace = torch.empty(max(expert_ffn_w8a8_workspace_size(rows, H, E, I), 256),
+                                    dtype=torch.uint8, device=x_perm.device)
+        _need(workspace, "workspace", torch.uint8)
+        _same_device(x_perm, offsets, fc1_q, fc1_scale, fc2_q, fc2_scale, fc1_bias, fc2_bias,
+                     y_perm, workspace)
+        check(_lib().moe_expert_ffn_w8a8(_ptr(x_perm), _ptr(offsets), _ptr(fc1_q), _ptr(fc1_scale),
+                                         _ptr(fc2_q), _ptr(fc2_scale), _ptr(fc1_bias),
+                                         _ptr(fc2_bias), rows, H, E, I, _swiglu(*swiglu),
+                                         _layout(fc1_layout), _ptr(y_perm), _ptr(workspace),
+                                         workspace.numel(), _stream(s)), "moe_expert_ffn_w8a8")
+    return y_perm
+
+
+def w8a8_workspace_size(T, H, E, k, I):
+    """Bytes of workspace forward_w8a8 needs (0 for sizes it rejects)."""
+    return _lib().moe_w8a8_workspace_size(T, H, E, k, I)
+
+
+def forward_w8a8(hidden, router_w, fc1_q, fc1_scale, fc2_q, fc2_scale, k, normalize=True,
+                 router_bias=None, out=None, workspace=None, stream=None,
+                 swiglu=(1.0, 0.0, float("inf")), fc1_bias=None, fc2_bias=None,
+                 fc1_layout="interleaved", norm_weight=None, norm_eps=1e-6):
+    """The layer with int8 experts and int8 activations in the expert products (the router
+    reads the bf16 input): arguments as forward_q8, any batch size."""
+    _need(hidden, "hidden", torch.bfloat16)
+    T, H = hidden.shape
+    E = router_w.shape[0]
+    I = fc2_q.shape[2]
+    _need(router_w, "router_w", torch.bfloat16, (E, H))
+    _q8(fc1_q, fc1_scale, "fc1", (E, 2 * I, H))
+    _q8(fc2_q, fc2_scale, "fc2", (E, H, I))
+    if router_bias is not None:
+        _need(router_bias, "router_bias", torch.float32, (E,))
+    _biases(fc1_bias, fc2_bias, torch.bfloat16, E, I, H)
+    if norm_weight is not None:
+        _need(norm_weight, "norm_weight", torch.bfloat16, (H,))
+    s, here = _on(hidden, stream)
+    with here:
+        if out is None:
+            out = torch.empty_like(hidden)
+        _need(out, "out", torch.bfloat16, (T, H))
+        if workspace is None:
+            workspace = torch.empty(max(w8a8_workspace_size(T, H, E, k, I), 256), dtype=torch.uint8,
+                                    device=hidden.device)
+        _need(workspace, "workspace", torch.uint8)
+        _same_device(hidden, router_w, router_bias, fc1_q, fc1_scale, fc2_q, fc2_scale, fc1_bias,
+                     fc2_bias, norm_weight, out, workspace)
+        check(_lib().moe_forward_w8a8(_ptr(hidden), _ptr(norm_weight), float(norm_eps),
+                                      _ptr(router_w), _ptr(router_bias), _ptr(fc1_q),
+                                      _ptr(fc1_scale), _ptr(fc2_q), _ptr(fc2_scale), _ptr(fc1_bias),
+                                      _ptr(fc2_bias), T, H, E, k, I, int(bool(normalize)),
+                                      _swiglu(*swiglu), _layout(fc1_layout), _ptr(out),
+                                      _ptr(workspace), workspace.numel(), _stream(s)),
+              "moe_forward_w8a8")
+    return out
+
+
+def _balance_batch(logits, mask, seq_offsets):
+    _need(logits, "logits", torch.float32)
+    T, E = logits.shape
+    if mask is not None:
+        if mask.dtype == torch.bool:
+            mask = mask.view(torch.uint8)
+        _need(mask, "mask", torch.uint8, (T,))
+    S = 1
+    if seq_offsets is not None:
+        _need(seq_offsets, "seq_offsets", torch.int32)
+        if seq_offsets.dim() != 1 or seq_offsets.numel() < 2:
+            raise ValueError("seq_offsets must be [S + 1] with S >= 1")
+        S = seq_offsets.numel() - 1
+    return T, E, S, mask
+
+
+def balance_loss(logits, topk_idx, coef=1.0, mask=None, seq_offsets=None, err_word=None,
+                 workspace=None, stream=None):
+    """Load-balance loss of a routing (route's logits and idx) and its per-expert counts:
+    with n valid tokens, f_e = counts_e / (n k) and P_e the mean softmax probability,
+    coef E sum_e f_e P_e, averaged over the sequences seq_offsets [S+1] cuts the batch
+    into (default: one).  mask [T] (bool or uint8): False leaves a token (padding) out.
+    Returns loss [1], counts [S, E] int32, probs [S, E] (P) and tokens [S] int32 (n)."""
+    T, E, S, mask = _balance_batch(logits, mask, seq_offsets)
+    _need(topk_idx, "topk_idx", torch.int32)
+    if topk_idx.dim() != 2 or topk_idx.shape[0] != T:
+        raise ValueError(f"topk_idx must be [{T}, k], got {tuple(topk_idx.shape)}")
+    if err_word is not None:
+        _need(err_word, "err_word", torch.int32)
+    s, here = _on(logits, stream)
+    dev = logits.device
+    with here:
+        loss = torch.empty((1,), dtype=torch.float32, device=dev)
+        counts = torch.empty((S, E), dtype=torch.int32, device=dev)
+        probs = torch.empty((S, E), dtype=torch.float32, device=dev)
+        tokens = torch.empty((S,), dtype=torch.int32, device=dev)
+        if workspace is None:
+            workspace = torch.empty(max(_lib().moe_balance_loss_workspace_size(T, E, S), 256),
+                                    dtype=torch.uint8, device=dev)
+        _need(workspace, "workspace", torch.uint8)
+        _same_device(logits, topk_idx, mask, seq_offsets, err_word, workspace)
+        check(_lib().moe_balance_loss(_ptr(logits), _ptr(topk_idx), _ptr(mask), _ptr(seq_offsets),
+                                      T, E, topk_idx.shape[1], S, float(coef), _ptr(loss),
+                                      _ptr(counts), _ptr(probs), _ptr(tokens), _ptr(err_word),
+                                      _ptr(workspace), workspace.numel(), _stream(s)),
+              "moe_balance_loss")
+    return dict(loss=loss, counts=counts, probs=probs, tokens=tokens)
+
+
+def balance_loss_backward(logits, k, counts, tokens, coef=1.0, mask=None, seq_offsets=None,
+                          grad_loss=None, dlogits=None, stream=None):
+    """Gradient of balance_loss with respect to the logits (the counts are constants), for
+    the same logits, coef, mask and seq_offsets and the counts and tokens it returned;
+    grad_loss [1] float32 is the gradient arriving at the loss (default 1).  Tokens that
+    take no part get zeros."""
+    T, E, S, mask = _balance_batch(logits, mask, seq_offsets)
+    _need(counts, "counts", torch.int32, (S, E))
+    _need(tokens, "tokens", torch.int32, (S,))
+    if grad_loss is not None:
+        _need(grad_loss, "grad_loss", torch.float32)
+        if grad_loss.numel() != 1:
+            raise ValueError("grad_loss must hold one value")
+    s, here = _on(logits, stream)
+    with here:
+        if dlogits is None:
+            dlogits = torch.empty_like(logits)
+        _need(dlogits, "dlogits", torch.float32, (T, E))
+        _same_device(logits, counts, tokens, mask, seq_offsets, grad_loss, dlogits)
+        check(_lib().moe_balance_loss_backward(_ptr(logits), _ptr(mask), _ptr(seq_offsets),
+                                               _ptr(counts), _ptr(tokens), T, E, int(k), S,
+                                               float(coef), _ptr(grad_loss), _ptr(dlogits),
+                                               _stream(s)), "moe_balance_loss_backward")
+    return dlogits
 
 
 def rmsnorm(x, weight, eps=1e-6, out=None, stream=None):

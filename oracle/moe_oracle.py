@@ -409,3 +409,84 @@ def chunked_to_interleaved(fc1_chunked: np.ndarray) -> np.ndarray:
         for s in (0, 1):
             dst[:, 2 * j + s] = src[:, s * I + j]
     return dst
+
+
+# ------------------------------------------------- int8 activations x int8 weights
+
+def quantize_rows(x):
+    """(q [rows, K] int64 in [-127, 127], scale [rows] float32): the whole number nearest
+    127 x / max|x| of the row, ties to even; scale = max|x| / 127 in float32.  Zero rows
+    give 0 and scale 0, rows with a NaN or an infinity 0 and scale NaN.  (127 x is exact in
+    float64 for float32 x, and the quotient is a half exactly or far from one.)"""
+    x = np.asarray(x, dtype=np.float64)
+    q = np.zeros(x.shape, dtype=np.int64)
+    scale = np.zeros(x.shape[0], dtype=np.float32)
+    for r in range(x.shape[0]):
+        if not np.all(np.isfinite(x[r])):
+            scale[r] = np.nan
+            continue
+        top = np.max(np.abs(x[r])) if x.shape[1] else 0.0
+        if top == 0.0:
+            continue
+        scale[r] = np.float32(top) / np.float32(127)
+        q[r] = np.rint(127.0 * x[r] / top).astype(np.int64)
+    return q, scale
+
+
+def matmul_q8(a_q, a_scale, w_q, w_scale, bias=None):
+    """(sum_k a_q[r, k] w_q[n, k]) a_scale[r] w_scale[n] + bias[n]: whole-number sums, the
+    rest float64."""
+    s = np.asarray(a_q, dtype=np.int64) @ np.asarray(w_q, dtype=np.int64).T
+    y = s.astype(np.float64) * np.asarray(a_scale, dtype=np.float64)[:, None] * \
+        np.asarray(w_scale, dtype=np.float64)[None, :]
+    return y if bias is None else y + np.asarray(bias, dtype=np.float64)[None, :]
+
+
+def expert_ffn_w8a8(x_rows, fc1_q, fc1_scale, fc2_q, fc2_scale, layout: str = "interleaved",
+                    act=STANDARD_SWIGLU, b1=None, b2=None) -> np.ndarray:
+    """One expert: rows to int8, product with fc1, SwiGLU, rows to int8, product with fc2."""
+    q, s = quantize_rows(x_rows)
+    h = matmul_q8(q, s, fc1_q, fc1_scale, b1)
+    gate, up = fc1_gate_up(h.T, layout)
+    a = swiglu(gate.T, up.T, *act)
+    q, s = quantize_rows(a)
+    return matmul_q8(q, s, fc2_q, fc2_scale, b2)
+
+
+# ------------------------------------------------------------------- load balance
+
+def balance_loss(logits, idx, coef=1.0, mask=None, seq_offsets=None):
+    """dict(loss, counts [S, E], probs [S, E], tokens [S], dlogits [T, E]): per sequence
+    f_e = counts_e / (n k), P_e the mean softmax probability, E sum f P; the mean over the
+    sequences times coef, and its gradient for constant counts."""
+    L = np.asarray(logits, dtype=np.float64)
+    idx = np.asarray(idx)
+    T, E = L.shape
+    k = idx.shape[1]
+    seq = [0, T] if seq_offsets is None else [int(v) for v in seq_offsets]
+    S = len(seq) - 1
+    valid = np.ones(T, dtype=bool) if mask is None else np.asarray(mask).astype(bool)
+    counts = np.zeros((S, E), dtype=np.int64)
+    probs = np.zeros((S, E))
+    tokens = np.zeros(S, dtype=np.int64)
+    grad = np.zeros((T, E))
+    loss = 0.0
+    for s in range(S):
+        ts = [t for t in range(seq[s], seq[s + 1]) if valid[t]]
+        tokens[s] = n = len(ts)
+        if n == 0:
+            continue
+        p = np.zeros((n, E))
+        for i, t in enumerate(ts):
+            if not np.all(L[t] == -np.inf):
+                ex = np.exp(L[t] - np.max(L[t]))
+                p[i] = ex / np.sum(ex)
+            for j in range(k):
+                if 0 <= idx[t, j] < E:
+                    counts[s, idx[t, j]] += 1
+        f = counts[s] / (n * k)
+        probs[s] = np.sum(p, axis=0) / n
+        loss += E * np.sum(f * probs[s])
+        for i, t in enumerate(ts):
+            grad[t] = coef * E / (S * n) * p[i] * (f - np.sum(f * p[i]))
+    return dict(loss=coef / S * loss, counts=counts, probs=probs, tokens=tokens, dlogits=grad)
