@@ -1,117 +1,655 @@
-// Grouped products of int8 rows with int8 weights, scales per token and per channel:
+// Products of int8 rows with int8 weights on the tensor cores (tcgen05 kind::i8), scales
+// per row and per channel, grouped by expert (one expert and no offsets: a dense product):
 //   out[r, n] = (sum_k a[r, k] w[e, n, k]) sa[r] sw[e, n] + bias[e, n]
-// for the rows r of expert e (one expert and no offsets: a dense product).  The sum is
-// exact in int32 (K <= 65536: |sum| <= 2^30); it is rounded to float32 once, scaled by the
-// product of the two scales and, after the bias, rounded once to the output's type.
-// With SwiGLU (fc1 of the expert FFN) the (gate, up) pairs of rows give one float32
-// activation each.
+// The sum is exact in int32 (K <= 65536: |sum| <= 2^30); it is rounded to float32 once,
+// scaled by the product of the two scales and, after the bias, rounded once to the output's
+// type.  With SwiGLU (fc1 of the expert FFN) the (gate, up) pairs of rows give one float32
+// activation each, not rounded further: it is cut to 8 bits next, and 16-bit activations
+// would move one in ten of those whole numbers.
+//
+// Both kernels put the WEIGHT rows on the MMA's M side and the tokens on N, so that a few
+// tokens cost a few columns, not a tile of rows:
+//   q8_stream_kernel  128 weight rows x up to 64 tokens per CTA: few rows per expert, each
+//                     weight byte read once, bound by HBM
+//   q8_pair_kernel    256 weight rows x up to 256 tokens per pair of CTAs: many rows per
+//                     expert, bound by the tensor cores
+#include <cuda.h>
+
 #include "common.cuh"
 #include "kernels.h"
+#include "sm100.cuh"
 #include "tile_map.cuh"
+#include "tmap.cuh"
 
 namespace moe {
 namespace {
 
-constexpr int QBM = 32, QBN = 64, QBK = 32;   // rows, columns, K words of 4 bytes
+using namespace sm100;
+
+constexpr int kBK = tmap::kBoxK8;    // K per ring slot: one 128-byte row
+constexpr uint64_t kWaitNs = 2000000000ull;
 
 enum OutMode : int { OUT_F32 = 0, OUT_BF16 = 1, OUT_SWIGLU = 2 };
 
+struct Q8Params {
+    const int32_t* offsets;   // [E+1] device, or nullptr: one group of `rows` rows
+    int E, rows, K, N;
+    const float* sa;          // [rows]
+    const float* sw;          // [E, N]
+    const void* bias;         // [E, N] or nullptr
+    void* out;                // [rows, N] (SwiGLU: [rows, N / 2] float32)
+    int32_t* err;
+    SwigluAttr act;
+    bool chunked;             // SwiGLU: scales and bias in the chunked layout
+};
+
+// Scale and bias of weight row wr (SwiGLU: in interleaved order) of expert g.
 template <int MODE>
-__global__ void __launch_bounds__(256)
-q8_gemm_kernel(const int8_t* __restrict__ A, const float* __restrict__ sa, const int8_t* __restrict__ W,
-               const float* __restrict__ sw, const void* __restrict__ bias, const int32_t* offsets,
-               int rows, int K, int E, int N, void* __restrict__ out, int32_t* err, SwigluAttr act,
-               bool chunked) {
-    __shared__ int sA[QBM][QBK + 1];
-    __shared__ __align__(16) int sW[QBK][QBN + 4];
-    __shared__ int s_off[kMaxExperts + 1];
-    __shared__ int s_pre[kMaxExperts + 1];
-    const int tid = threadIdx.x;
+__device__ __forceinline__ void channel(const Q8Params& p, int g, int wr, float* scale, float* bias) {
+    const int row = MODE == OUT_SWIGLU ? fc1_row(wr, p.N / 2, p.chunked) : wr;
+    const size_t i = static_cast<size_t>(g) * p.N + row;
+    *scale = p.sw[i];
+    *bias = 0.f;
+    if (p.bias)
+        *bias = MODE == OUT_F32 ? static_cast<const float*>(p.bias)[i]
+                                : bf16_at(static_cast<const __nv_bfloat16*>(p.bias), i);
+}
+
+// Output of one weight row (a lane; SwiGLU: gate rows on even lanes, up rows on odd ones)
+// and one token; called by whole warps.
+template <int MODE>
+__device__ __forceinline__ void store_one(const Q8Params& p, int row, int wr, float y, bool valid) {
+    if constexpr (MODE == OUT_SWIGLU) {
+        const float up = __shfl_xor_sync(0xffffffffu, y, 1);
+        if (valid && !(wr & 1))
+            static_cast<float*>(p.out)[static_cast<size_t>(row) * (p.N / 2) + (wr >> 1)] = swiglu_attr(y, up, p.act);
+    } else if (valid) {
+        const size_t o = static_cast<size_t>(row) * p.N + wr;
+        if constexpr (MODE == OUT_BF16) static_cast<__nv_bfloat16*>(p.out)[o] = __float2bfloat16_rn(y);
+        else static_cast<float*>(p.out)[o] = y;
+    }
+}
+
+// --------------------------------------------------------------------- few rows: stream
+// Six warps a CTA: 0 the TMA producer, 1 the MMA issuer, 2-5 the epilogue (warp w reads
+// tensor-memory lanes 32 (w % 4) .. +31, one weight row a lane).  Units (64-token chunk x
+// 128 weight rows) are strided over the clusters.  A cluster of CS CTAs shares one unit
+// along K when there are too few units for the SMs (one unit a cluster then): every CTA
+// accumulates its slices, sends its partial sums to the CTA that owns those tokens (whole
+// numbers: any order gives the same sum) and finishes its own tokens.
+constexpr int kSTok = 64;                       // tokens per chunk
+constexpr int kSBox = 16;                       // token rows per TMA box
+constexpr int kSWRows = 128;
+constexpr int kSSub = 2;                        // slots per barrier stage
+constexpr int kSMaxStages = 4;
+// ring slots: what fits (a split unit has few K slices a CTA, and needs room for the sums)
+__host__ __device__ constexpr int stream_slots(bool split) { return kSSub * (split ? 3 : kSMaxStages); }
+constexpr int kSABytes = kSWRows * kBK;
+constexpr int kSBBytes = kSTok * kBK;
+constexpr int kSThreads = 192;
+constexpr int kSPartBytes = kSWRows * kSTok * 4;   // partial sums of one unit (CS > 1)
+constexpr int kSMiscBytes = (2 * kSMaxStages + 4) * 8 + 16 + 2 * (kMaxExperts + 1) * 4 + 64;
+
+constexpr int stream_smem(bool split) {
+    return 1024 + stream_slots(split) * (kSABytes + kSBBytes) + (split ? kSPartBytes : 0) + kSMiscBytes;
+}
+static_assert(stream_smem(true) <= 227 * 1024, "shared memory");
+
+template <int MODE, bool SPLIT>
+__global__ void __launch_bounds__(kSThreads, 1)
+q8_stream_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
+                 const Q8Params p, const int cs) {
+    constexpr int kSSlots = stream_slots(SPLIT), kSStages = kSSlots / kSSub;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                               ~static_cast<uintptr_t>(1023));
+    uint8_t* sA = smem;
+    uint8_t* sB = smem + kSSlots * kSABytes;
+    int* s_part = reinterpret_cast<int*>(sB + kSSlots * kSBBytes);   // SPLIT
+    uint64_t* full = reinterpret_cast<uint64_t*>(sB + kSSlots * kSBBytes + (SPLIT ? kSPartBytes : 0));
+    uint64_t* empty = full + kSStages;
+    uint64_t* tfull = empty + kSStages;
+    uint64_t* tempty = tfull + 2;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tempty + 2);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    int* s_off = reinterpret_cast<int*>(tmem_slot + 4);
+    int* s_pre = s_off + (kMaxExperts + 1);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = SPLIT ? static_cast<int>(cluster_ctarank()) : 0;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kSStages; ++s) {
+            mbar_init(smem_u32(&full[s]), 1);
+            mbar_init(smem_u32(&empty[s]), 1);
+        }
+        for (int a = 0; a < 2; ++a) {
+            mbar_init(smem_u32(&tfull[a]), 1);
+            mbar_init(smem_u32(&tempty[a]), 4);
+        }
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 0 && lane == 0) {
+        tma_prefetch_desc(&tmW);
+        tma_prefetch_desc(&tmX);
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_u32(tmem_slot), 2 * kSTok);
+        tmem_relinquish();
+    }
+    // the prologue above touches no global memory; everything below may
     pdl_wait();
     pdl_trigger();
-    if (tid < 32) build_group_tiles(offsets, rows, err, E, QBM, s_off, s_pre, tid);
+    if (warp == 2) build_group_tiles(p.offsets, p.rows, p.err, p.E, kSTok, s_off, s_pre, lane);
+    tc_fence_before();
     __syncthreads();
-    const int NT = (N + QBN - 1) / QBN;
-    const long long total = static_cast<long long>(s_pre[E]) * NT;
-    const int tx = tid & 15, ty = tid >> 4;
-    const int KW = K / 4;
-    for (long long u = blockIdx.x; u < total; u += gridDim.x) {
-        const int mt = static_cast<int>(u / NT), nt = static_cast<int>(u - static_cast<long long>(mt) * NT);
-        const int e = tile_group(mt, E, s_pre);
-        const int row0 = s_off[e] + (mt - s_pre[e]) * QBM;
-        const int nrows = min(QBM, s_off[e + 1] - row0);
-        const int* We = reinterpret_cast<const int*>(W) + static_cast<size_t>(e) * N * KW;
-        const int* Aw = reinterpret_cast<const int*>(A);
-        int acc[2][4] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
-        for (int k0 = 0; k0 < KW; k0 += QBK) {
-            for (int i = tid; i < QBM * QBK; i += 256) {
-                const int r = i / QBK, c = i % QBK;
-                sA[r][c] = (r < nrows && k0 + c < KW) ? Aw[static_cast<size_t>(row0 + r) * KW + k0 + c] : 0;
-            }
-            for (int i = tid; i < QBN * QBK; i += 256) {
-                const int n = i / QBK, c = i % QBK, wn = nt * QBN + n;
-                const int wr = MODE == OUT_SWIGLU ? fc1_row(wn, N / 2, chunked) : wn;
-                sW[c][n] = (wn < N && k0 + c < KW) ? We[static_cast<size_t>(wr) * KW + k0 + c] : 0;
-            }
-            __syncthreads();
-#pragma unroll 8
-            for (int c = 0; c < QBK; ++c) {
-                const int a0 = sA[ty * 2][c], a1 = sA[ty * 2 + 1][c];
-                const int4 w4 = *reinterpret_cast<const int4*>(&sW[c][tx * 4]);
-                const int w[4] = {w4.x, w4.y, w4.z, w4.w};
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    acc[0][j] = __dp4a(a0, w[j], acc[0][j]);
-                    acc[1][j] = __dp4a(a1, w[j], acc[1][j]);
+    if (SPLIT) cluster_sync();
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+
+    const int MT = (p.N + kSWRows - 1) / kSWRows;
+    const long long units = static_cast<long long>(s_pre[p.E]) * MT;
+    const int first = static_cast<int>(blockIdx.x) / cs, step = static_cast<int>(gridDim.x) / cs;
+    const int nk_all = (p.K + kBK - 1) / kBK;
+    const int kb_lo = static_cast<int>(static_cast<long long>(rank) * nk_all / cs);
+    const int kb_hi = static_cast<int>(static_cast<long long>(rank + 1) * nk_all / cs);
+
+    auto unit = [&](long long u, int* g, int* row0, int* nrows) {
+        const int tile = static_cast<int>(u / MT);
+        *g = tile_group(tile, p.E, s_pre);
+        *row0 = s_off[*g] + (tile - s_pre[*g]) * kSTok;
+        *nrows = min(kSTok, s_off[*g + 1] - *row0);
+        return static_cast<int>(u - static_cast<long long>(tile) * MT);
+    };
+
+    if (warp == 0) {
+        int stage = 0;
+        uint32_t phase = 0;
+        for (long long u = first; u < units && !*abort_flag; u += step) {
+            int g, row0, nrows;
+            const int mt = unit(u, &g, &row0, &nrows);
+            const int nl = (nrows + kSBox - 1) / kSBox;
+            const uint32_t bytes = static_cast<uint32_t>(kSABytes + nl * kSBox * kBK);
+            bool ok = true;
+            for (int kb0 = kb_lo; kb0 < kb_hi; kb0 += kSSub) {
+                const int ns = min(kSSub, kb_hi - kb0);
+                if (lane == 0) {
+                    ok = mbar_wait(smem_u32(&empty[stage]), phase ^ 1u, abort_flag, kWaitNs);
+                    if (ok) mbar_arrive_expect_tx(smem_u32(&full[stage]), static_cast<uint32_t>(ns) * bytes);
+                }
+                ok = __shfl_sync(0xffffffffu, ok, 0);
+                if (!ok) break;
+                const uint32_t fb = smem_u32(&full[stage]);
+                for (int j = 0; j < ns; ++j) {
+                    const int sl = stage * kSSub + j, k0 = (kb0 + j) * kBK;
+                    if (lane == 0) tma_load_4d(smem_u32(sA + sl * kSABytes), &tmW, fb, k0, 0, mt * (kSWRows / 2), g);
+                    if (lane < nl)
+                        tma_load_2d(smem_u32(sB + sl * kSBBytes) + lane * kSBox * kBK, &tmX, fb, k0, row0 + lane * kSBox);
+                }
+                if (++stage == kSStages) {
+                    stage = 0;
+                    phase ^= 1u;
                 }
             }
-            __syncthreads();
+            if (!ok) break;
         }
-        const int n0 = nt * QBN + tx * 4;
-        if (n0 >= N) continue;   // N is a multiple of 4: a thread's columns are all valid or none
+    } else if (warp == 1) {
+        if (lane == 0) {
+            int stage = 0, acc = 0;
+            uint32_t phase = 0, acc_phase = 0;
+            for (long long u = first; u < units && !*abort_flag; u += step) {
+                int g, row0, nrows;
+                unit(u, &g, &row0, &nrows);
+                const uint32_t idesc = idesc_s8_s32(kSWRows, ((nrows + 15) / 16) * 16);
+                if (!mbar_wait(smem_u32(&tempty[acc]), acc_phase ^ 1u, abort_flag, kWaitNs)) break;
+                tc_fence_after();
+                const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * kSTok);
+                bool ok = true;
+                for (int kb0 = kb_lo; kb0 < kb_hi; kb0 += kSSub) {
+                    const int ns = min(kSSub, kb_hi - kb0);
+                    if (!mbar_wait(smem_u32(&full[stage]), phase, abort_flag, kWaitNs)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    for (int j = 0; j < ns; ++j) {
+                        const int sl = stage * kSSub + j;
+                        const uint32_t a0 = smem_u32(sA + sl * kSABytes), b0 = smem_u32(sB + sl * kSBBytes);
 #pragma unroll
-        for (int rr = 0; rr < 2; ++rr) {
-            const int r = ty * 2 + rr;
-            if (r >= nrows) continue;
-            const float s = sa[row0 + r];
-            float y[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int wr = MODE == OUT_SWIGLU ? fc1_row(n0 + j, N / 2, chunked) : n0 + j;
-                const size_t wi = static_cast<size_t>(e) * N + wr;
-                float b = 0.f;
-                if (bias) b = MODE == OUT_F32 ? static_cast<const float*>(bias)[wi]
-                                              : bf16_at(static_cast<const __nv_bfloat16*>(bias), wi);
-                y[j] = fmaf(static_cast<float>(acc[rr][j]), s * sw[wi], b);
-            }
-            const size_t o = static_cast<size_t>(row0 + r) * (MODE == OUT_SWIGLU ? N / 2 : N);
-            if constexpr (MODE == OUT_SWIGLU) {
-                *reinterpret_cast<float2*>(static_cast<float*>(out) + o + n0 / 2) =
-                    make_float2(swiglu_attr(y[0], y[1], act), swiglu_attr(y[2], y[3], act));
-            } else if constexpr (MODE == OUT_BF16) {
-                *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(out) + o + n0) =
-                    make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
-            } else {
-                *reinterpret_cast<float4*>(static_cast<float*>(out) + o + n0) =
-                    make_float4(y[0], y[1], y[2], y[3]);
+                        for (int kk = 0; kk < kBK / 32; ++kk)
+                            umma_s8(d_tmem, smem_desc_sw128(a0 + kk * 32), smem_desc_sw128(b0 + kk * 32), idesc,
+                                    (kb0 + j > kb_lo || kk > 0) ? 1u : 0u);
+                    }
+                    umma_commit(smem_u32(&empty[stage]));
+                    if (++stage == kSStages) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+                if (!ok) break;
+                umma_commit(smem_u32(&tfull[acc]));
+                acc ^= 1;
+                if (acc == 0) acc_phase ^= 1u;
             }
         }
     }
+    const int quad = warp & 3, r = quad * 32 + lane;
+    if (warp >= 2) {
+        int acc = 0;
+        uint32_t acc_phase = 0;
+        for (long long u = first; u < units && !*abort_flag; u += step) {
+            int g, row0, nrows;
+            const int mt = unit(u, &g, &row0, &nrows);
+            const int wr = mt * kSWRows + r;
+            const bool wvalid = wr < p.N;   // N is even: a (gate, up) pair is valid or not as one
+            float sw = 0.f, bias = 0.f;
+            if (!SPLIT && wvalid) channel<MODE>(p, g, wr, &sw, &bias);
+            if (!mbar_wait(smem_u32(&tfull[acc]), acc_phase, abort_flag, kWaitNs)) break;
+            tc_fence_after();
+            const uint32_t tb = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + static_cast<uint32_t>(acc * kSTok);
+#pragma unroll 1
+            for (int c = 0; c < nrows; c += 16) {
+                uint32_t v[16];
+                tmem_ld_32x32b_x16(tb + c, v);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const int n = c + i;
+                    if constexpr (SPLIT) {
+                        const int per = kSTok / cs, dst = n / per;
+                        const uint32_t at = smem_u32(s_part + (rank * per + n - dst * per) * kSWRows + r);
+                        if (n < nrows)
+                            st_shared_cluster_s32(mapa_shared(at, static_cast<uint32_t>(dst)), static_cast<int>(v[i]));
+                    } else {
+                        const float sa = p.sa[row0 + min(n, nrows - 1)];
+                        const float y = fmaf(static_cast<float>(static_cast<int>(v[i])), sa * sw, bias);
+                        store_one<MODE>(p, row0 + n, wr, y, n < nrows && wvalid);
+                    }
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&tempty[acc]));
+            acc ^= 1;
+            if (acc == 0) acc_phase ^= 1u;
+        }
+    }
+    if constexpr (SPLIT) {
+        __syncwarp();
+        cluster_sync();   // every partial sum of the cluster's unit has arrived
+        if (warp >= 2 && first < units) {
+            int g, row0, nrows;
+            const int mt = unit(first, &g, &row0, &nrows);
+            const int wr = mt * kSWRows + r, per = kSTok / cs;
+            const bool wvalid = wr < p.N;
+            float sw = 0.f, bias = 0.f;
+            if (wvalid) channel<MODE>(p, g, wr, &sw, &bias);
+            for (int n = rank * per; n < min((rank + 1) * per, nrows); ++n) {
+                int sum = 0;
+                for (int q = 0; q < cs; ++q) sum += s_part[(q * per + n - rank * per) * kSWRows + r];
+                store_one<MODE>(p, row0 + n, wr, fmaf(static_cast<float>(sum), p.sa[row0 + n] * sw, bias), wvalid);
+            }
+        }
+    }
+    if (*abort_flag) {
+        // copies already issued may still land: give them time before the CTA exits
+        const uint64_t t0 = global_timer_ns();
+        while (global_timer_ns() - t0 < 200000ull) __nanosleep(1000);
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem_base, 2 * kSTok);
+    }
+    if (threadIdx.x == 0 && *abort_flag && p.err) atomicOr(p.err, kErrTimeout);
+}
+
+// --------------------------------------------------------------------- many rows: pairs
+// A cluster of two CTAs runs one unit (expert, up to 256 tokens, 256 weight rows) as one
+// M = 256 MMA: each CTA loads its own 128 weight rows and half of the tokens, and holds its
+// 128 weight rows x all tokens of the unit in tensor memory (two accumulators of 256
+// columns).  The weight rows are loaded in fragment order (lane 8 q + j of a 32-lane
+// quadrant holds the quadrant's row 4 j + q), so that a 16x256b accumulator fragment gives a
+// thread four consecutive weight rows of two tokens, stored straight from registers.
+// Ten warps a CTA: 0 the TMA producer, 1 the MMA issuer (even CTA), 2-9 the epilogue.
+constexpr int kPThreads = 320;
+constexpr int kPWRows = 128;
+constexpr int kPTok = 256;
+constexpr int kPSlots = 6;
+constexpr int kPSub = 2;
+constexpr int kPStages = kPSlots / kPSub;
+constexpr int kPABytes = kPWRows * kBK;
+constexpr int kPBox = kPTok / 2;
+constexpr int kPBBytes = kPBox * kBK;
+constexpr int kPAccCols = 256;
+constexpr int kPMiscBytes = (2 * kPStages + 4) * 8 + 16 + 2 * (kMaxExperts + 1) * 4 + 64;
+constexpr int kPSmemBytes = 1024 + kPSlots * (kPABytes + kPBBytes) + kPMiscBytes;
+static_assert(kPSmemBytes <= 227 * 1024, "shared memory");
+
+struct PUnit {
+    int g, row0, nrows, n, mt;   // expert, first row, rows, MMA N, weight tile
+};
+
+__device__ __forceinline__ PUnit pair_unit(long long u, int MT, int G, const int* s_off, const int* s_pre) {
+    PUnit d;
+    const int tile = static_cast<int>(u / MT);
+    d.mt = static_cast<int>(u - static_cast<long long>(tile) * MT);
+    d.g = tile_group(tile, G, s_pre);
+    d.row0 = s_off[d.g] + (tile - s_pre[d.g]) * kPTok;
+    d.nrows = min(kPTok, s_off[d.g + 1] - d.row0);
+    d.n = ((d.nrows + 31) / 32) * 32;   // each CTA's half: a multiple of 16 rows
+    return d;
+}
+
+template <int MODE>
+__global__ void __launch_bounds__(kPThreads, 1)
+q8_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
+               const Q8Params p) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                               ~static_cast<uintptr_t>(1023));
+    uint8_t* sA = smem;
+    uint8_t* sB = smem + kPSlots * kPABytes;
+    uint64_t* full = reinterpret_cast<uint64_t*>(sB + kPSlots * kPBBytes);
+    uint64_t* empty = full + kPStages;
+    uint64_t* tfull = empty + kPStages;
+    uint64_t* tempty = tfull + 2;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tempty + 2);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    int* s_off = reinterpret_cast<int*>(tmem_slot + 4);
+    int* s_pre = s_off + (kMaxExperts + 1);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank();
+    const bool lead = rank == 0;
+    const int G = p.E;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kPStages; ++s) {
+            mbar_init(smem_u32(&full[s]), 1);    // the even CTA's producer (expect_tx)
+            mbar_init(smem_u32(&empty[s]), 1);   // the pair MMA's commit
+        }
+        for (int a = 0; a < 2; ++a) {
+            mbar_init(smem_u32(&tfull[a]), 1);
+            mbar_init(smem_u32(&tempty[a]), 16); // 8 epilogue warps x 2 CTAs
+        }
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 0 && lane == 0) {
+        tma_prefetch_desc(&tmW);
+        tma_prefetch_desc(&tmX);
+    }
+    if (warp == 1) {
+        tmem_alloc_pair(smem_u32(tmem_slot), 2 * kPAccCols);
+        tmem_relinquish_pair();
+    }
+    // the prologue above touches no global memory; everything below may
+    pdl_wait();
+    pdl_trigger();
+    if (warp == 2) build_group_tiles(p.offsets, p.rows, p.err, G, kPTok, s_off, s_pre, lane);
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();   // both CTAs' barriers and tensor memory exist before any signal
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+
+    const int MT = (p.N + 2 * kPWRows - 1) / (2 * kPWRows);
+    const long long units = static_cast<long long>(s_pre[G]) * MT;
+    const int pair = static_cast<int>(blockIdx.x >> 1), npairs = static_cast<int>(gridDim.x >> 1);
+    const int nk = (p.K + kBK - 1) / kBK;
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ TMA producer
+        int stage = 0;
+        uint32_t phase = 0;
+        for (long long u = pair; u < units && !*abort_flag; u += npairs) {
+            const PUnit d = pair_unit(u, MT, G, s_off, s_pre);
+            const int trow0 = d.row0 + static_cast<int>(rank) * (d.n / 2);
+            // weight views: plain (k, j, q, Q, e) at (k, 0, 0, w_in / 32, g); chunked fc1
+            // (k, j, s, qq, X) at (k, 0, 0, 0, g I / 8 + w_in / 32)
+            const int w_in = d.mt * 2 * kPWRows + static_cast<int>(rank) * kPWRows;
+            const bool chunked = MODE == OUT_SWIGLU && p.chunked;
+            const int wc3 = chunked ? 0 : w_in / 32;
+            const int wc4 = chunked ? d.g * (p.N / 16) + w_in / 32 : d.g;
+            const uint32_t bytes = static_cast<uint32_t>(2 * (kPABytes + kPBBytes));
+            bool ok = true;
+            for (int kb0 = 0; kb0 < nk; kb0 += kPSub) {
+                const int ns = min(kPSub, nk - kb0);
+                if (lane == 0) {
+                    ok = mbar_wait(smem_u32(&empty[stage]), phase ^ 1u, abort_flag, kWaitNs);
+                    if (ok && lead) mbar_arrive_expect_tx(smem_u32(&full[stage]), static_cast<uint32_t>(ns) * bytes);
+                }
+                ok = __shfl_sync(0xffffffffu, ok, 0);
+                if (!ok) break;
+                const uint32_t fb = mapa_shared(smem_u32(&full[stage]), 0);   // the even CTA's
+                if (lane == 0) {
+                    for (int j = 0; j < ns; ++j) {
+                        const int sl = stage * kPSub + j, k0 = (kb0 + j) * kBK;
+                        tma_load_5d_pair(smem_u32(sA + sl * kPABytes), &tmW, fb, k0, 0, 0, wc3, wc4);
+                        tma_load_2d_pair(smem_u32(sB + sl * kPBBytes), &tmX, fb, k0, trow0);
+                    }
+                }
+                if (++stage == kPStages) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
+            if (!ok) break;
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ MMA issuer
+        if (lead && lane == 0) {
+            int stage = 0, acc = 0;
+            uint32_t phase = 0, acc_phase = 0;
+            for (long long u = pair; u < units && !*abort_flag; u += npairs) {
+                const PUnit d = pair_unit(u, MT, G, s_off, s_pre);
+                const uint32_t idesc = idesc_s8_s32(2 * kPWRows, d.n);
+                if (!mbar_wait(smem_u32(&tempty[acc]), acc_phase ^ 1u, abort_flag, kWaitNs)) break;
+                tc_fence_after();
+                const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * kPAccCols);
+                bool ok = true;
+                for (int kb0 = 0; kb0 < nk; kb0 += kPSub) {
+                    const int ns = min(kPSub, nk - kb0);
+                    if (!mbar_wait(smem_u32(&full[stage]), phase, abort_flag, kWaitNs)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    for (int j = 0; j < ns; ++j) {
+                        const int sl = stage * kPSub + j;
+                        const uint32_t a0 = smem_u32(sA + sl * kPABytes), b0 = smem_u32(sB + sl * kPBBytes);
+#pragma unroll
+                        for (int kk = 0; kk < kBK / 32; ++kk)
+                            umma_s8_pair(d_tmem, smem_desc_sw128(a0 + kk * 32), smem_desc_sw128(b0 + kk * 32), idesc,
+                                         (kb0 + j > 0 || kk > 0) ? 1u : 0u);
+                    }
+                    umma_commit_pair(smem_u32(&empty[stage]), 0x3);
+                    if (++stage == kPStages) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+                if (!ok) break;
+                umma_commit_pair(smem_u32(&tfull[acc]), 0x3);
+                acc ^= 1;
+                if (acc == 0) acc_phase ^= 1u;
+            }
+        }
+    } else {
+        // ------------------------------------------------------------ epilogue
+        // Thread (fj, ft) = (lane / 4, lane % 4) of a 16x256b fragment holds weight rows
+        // 4 fj .. 4 fj + 3 of its quadrant for tokens 8 m + 2 ft + e of a 32-token chunk.
+        const int quad = warp & 3;
+        const int part = (warp - 2) >> 2;
+        const int fj = lane >> 2, ft = lane & 3;
+        int acc = 0;
+        uint32_t acc_phase = 0;
+        for (long long u = pair; u < units && !*abort_flag; u += npairs) {
+            const PUnit d = pair_unit(u, MT, G, s_off, s_pre);
+            const int w0 = d.mt * 2 * kPWRows + static_cast<int>(rank) * kPWRows + quad * 32;
+            const bool wvalid = w0 < p.N;   // N is a multiple of 32: the warp's rows are all valid or none
+            const int wr = w0 + 4 * fj;
+            float sw[4] = {0.f, 0.f, 0.f, 0.f}, bias[4] = {0.f, 0.f, 0.f, 0.f};
+            if (wvalid) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) channel<MODE>(p, d.g, wr + q, &sw[q], &bias[q]);
+            }
+            if (!mbar_wait(smem_u32(&tfull[acc]), acc_phase, abort_flag, kWaitNs)) break;
+            tc_fence_after();
+            const uint32_t tb = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) +
+                                static_cast<uint32_t>(acc * kPAccCols);
+#pragma unroll 1
+            for (int c = part * 32; c < d.nrows; c += 64) {
+                uint32_t lo[16], hi[16];
+                tmem_ld_16x256b_x4(tb + c, lo);                  // rows 4 fj, 4 fj + 1
+                tmem_ld_16x256b_x4(tb + (16u << 16) + c, hi);    // rows 4 fj + 2, 4 fj + 3
+                float sa[8];
+#pragma unroll
+                for (int m = 0; m < 4; ++m)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        sa[2 * m + e] = __ldg(p.sa + d.row0 + min(c + 8 * m + 2 * ft + e, d.nrows - 1));
+                tmem_wait_ld();
+                if (!wvalid) continue;
+#pragma unroll
+                for (int m = 0; m < 4; ++m) {
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int tok = c + 8 * m + 2 * ft + e;
+                        const float s = sa[2 * m + e];
+                        const float x0 = fmaf(static_cast<float>(static_cast<int>(lo[4 * m + e])), s * sw[0], bias[0]);
+                        const float x1 = fmaf(static_cast<float>(static_cast<int>(lo[4 * m + 2 + e])), s * sw[1], bias[1]);
+                        const float x2 = fmaf(static_cast<float>(static_cast<int>(hi[4 * m + e])), s * sw[2], bias[2]);
+                        const float x3 = fmaf(static_cast<float>(static_cast<int>(hi[4 * m + 2 + e])), s * sw[3], bias[3]);
+                        if (tok < d.nrows) {
+                            const size_t row = static_cast<size_t>(d.row0 + tok);
+                            if constexpr (MODE == OUT_SWIGLU)
+                                *reinterpret_cast<float2*>(static_cast<float*>(p.out) + row * (p.N / 2) + (wr >> 1)) =
+                                    make_float2(swiglu_attr(x0, x1, p.act), swiglu_attr(x2, x3, p.act));
+                            else if constexpr (MODE == OUT_BF16)
+                                *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + row * p.N + wr) =
+                                    make_uint2(pack_bf16x2(x0, x1), pack_bf16x2(x2, x3));
+                            else
+                                *reinterpret_cast<float4*>(static_cast<float*>(p.out) + row * p.N + wr) =
+                                    make_float4(x0, x1, x2, x3);
+                        }
+                    }
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&tempty[acc]), 0));
+            acc ^= 1;
+            if (acc == 0) acc_phase ^= 1u;
+        }
+    }
+
+    if (*abort_flag) {
+        // copies already issued may still land: give them time before the pair exits
+        const uint64_t t0 = global_timer_ns();
+        while (global_timer_ns() - t0 < 200000ull) __nanosleep(1000);
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();   // no CTA leaves while its partner may still read its memory
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc_pair(tmem_base, 2 * kPAccCols);
+    }
+    if (threadIdx.x == 0 && *abort_flag && p.err) atomicOr(p.err, kErrTimeout);
+}
+
+// ------------------------------------------------------------------------ host side
+
+// Launch in clusters of `cs` CTAs, programmatic stream serialisation allowed.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_clusters(void (*kern)(KArgs...), int ctas, int cs, int threads, int smem, cudaStream_t s,
+                            Args&&... args) {
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(cs);
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = cs > 1 ? 2 : 1;
+    count_launch();
+    return cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
+}
+
+// The kernel's shared-memory limit, once per device.
+template <typename K>
+cudaError_t set_smem(K* kern, int bytes, bool* done) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (done[dev]) return cudaSuccess;
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done[dev] = true;
+    return e;
+}
+
+template <int MODE, bool SPLIT>
+cudaError_t launch_stream(const CUtensorMap& w, const CUtensorMap& x, const Q8Params& p, int clusters, int cs,
+                          cudaStream_t s) {
+    static bool done[64] = {false};
+    const cudaError_t e = set_smem(q8_stream_kernel<MODE, SPLIT>, stream_smem(SPLIT), done);
+    if (e != cudaSuccess) return e;
+    return launch_clusters(q8_stream_kernel<MODE, SPLIT>, clusters * cs, cs, kSThreads, stream_smem(SPLIT), s, w, x, p, cs);
+}
+
+template <int MODE>
+cudaError_t launch_pair(const CUtensorMap& w, const CUtensorMap& x, const Q8Params& p, long long units, cudaStream_t s) {
+    static bool done[64] = {false};
+    const cudaError_t e = set_smem(q8_pair_kernel<MODE>, kPSmemBytes, done);
+    if (e != cudaSuccess) return e;
+    const long long most = device_sm_count() / 2;
+    return launch_clusters(q8_pair_kernel<MODE>, static_cast<int>(2 * (units < most ? units : most)), 2, kPThreads,
+                           kPSmemBytes, s, w, x, p);
+}
+
+// Rows per expert up to which the streaming kernel runs (a chunk of it).
+constexpr int kStreamRows = kSTok;
+
+template <int MODE>
+cudaError_t product(const Q8GemmArgs& a, const Q8Params& p, cudaStream_t s) {
+    CUtensorMap w, x;
+    const bool chunked = a.swiglu && a.fc1_chunked;
+    if (static_cast<long long>(a.rows) > static_cast<long long>(kStreamRows) * a.E) {
+        if (!tmap::quads8(&w, a.w_q, a.E, a.N, a.K, chunked)) return cudaErrorInvalidValue;
+        if (!tmap::matrix8(&x, a.a_q, a.rows, a.K, kPBox)) return cudaErrorInvalidValue;
+        const long long units = (static_cast<long long>((a.rows + kPTok - 1) / kPTok) + a.E) *
+                                ((a.N + 2 * kPWRows - 1) / (2 * kPWRows));
+        return launch_pair<MODE>(w, x, p, units, s);
+    }
+    if (!tmap::pairs8(&w, a.w_q, a.E, a.N, a.K, kSWRows / 2, chunked)) return cudaErrorInvalidValue;
+    if (!tmap::matrix8(&x, a.a_q, a.rows, a.K, kSBox)) return cudaErrorInvalidValue;
+    // chunks: at most one per row, and one per 64 rows and one more for every expert
+    // (dense: no more)
+    long long chunks = (a.rows + kSTok - 1) / kSTok;
+    if (a.offsets) chunks = a.rows < chunks + a.E ? a.rows : chunks + a.E;
+    const long long units = chunks * ((a.N + kSWRows - 1) / kSWRows);
+    const int sms = device_sm_count(), nk = (a.K + kBK - 1) / kBK;
+    int cs = 8;
+    while (cs > 1 && (units * cs > sms || cs > nk)) cs /= 2;
+    if (cs > 1) return launch_stream<MODE, true>(w, x, p, static_cast<int>(units), cs, s);
+    return launch_stream<MODE, false>(w, x, p, static_cast<int>(units < sms ? units : sms), 1, s);
 }
 
 }  // namespace
 
 cudaError_t launch_q8_gemm(const Q8GemmArgs& a, cudaStream_t s) {
     if (a.rows <= 0) return cudaSuccess;
-    const long long bound = (static_cast<long long>((a.rows + QBM - 1) / QBM) + a.E) * ((a.N + QBN - 1) / QBN);
-    const long long cap = static_cast<long long>(device_sm_count()) * 8;
-    const dim3 grid(static_cast<unsigned>(bound < cap ? bound : cap)), block(256);
-    auto go = [&](auto kern) {
-        return launch_k(kern, grid, block, 0, s, a.a_q, a.a_scale, a.w_q, a.w_scale, a.bias, a.offsets,
-                        a.rows, a.K, a.E, a.N, a.out, a.err, a.act, a.fc1_chunked);
-    };
-    if (a.swiglu) return go(q8_gemm_kernel<OUT_SWIGLU>);
-    return a.out_bf16 ? go(q8_gemm_kernel<OUT_BF16>) : go(q8_gemm_kernel<OUT_F32>);
+    const Q8Params p{a.offsets, a.E, a.rows, a.K, a.N, a.a_scale, a.w_scale, a.bias, a.out, a.err, a.act,
+                     a.fc1_chunked};
+    if (a.swiglu) return product<OUT_SWIGLU>(a, p, s);
+    return a.out_bf16 ? product<OUT_BF16>(a, p, s) : product<OUT_F32>(a, p, s);
 }
 
 }  // namespace moe

@@ -41,6 +41,7 @@ struct View {
     cuuint32_t box[5] = {0, 0, 0, 0, 0};
     int elem_bytes = 2;
     bool u8 = false;                // uint8 with the 64-byte swizzle, else bf16 with the 128-byte one
+    bool wide = false;              // u8: 128-byte box rows with the 128-byte swizzle
 };
 
 inline bool encode(CUtensorMap* m, const View& v, const void* ptr) {
@@ -50,7 +51,7 @@ inline bool encode(CUtensorMap* m, const View& v, const void* ptr) {
     return enc(m, v.u8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
                static_cast<cuuint32_t>(v.rank), const_cast<void*>(ptr), v.dims, v.strides, v.box,
                estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-               v.u8 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+               v.u8 && !v.wide ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -199,6 +200,58 @@ inline bool fc1_quad_rows_chunked_view(View* v, int E, int I, int K) {
 inline bool fc1_quad_rows_chunked(CUtensorMap* m, const void* fc1, int E, int I, int K) {
     View v;
     return fc1_quad_rows_chunked_view(&v, E, I, K) && encode(m, v, fc1);
+}
+
+// int8 operands of the int8 x int8 products: the bf16 views above with one byte an element
+// and boxes of 128 elements on K, so that a box row is the same 128 bytes with the same
+// swizzle.  K not a multiple of 128: the last box reads zeros past K.
+constexpr int kBoxK8 = 128;
+
+inline void narrow(View* v, int K) {
+    v->u8 = true;
+    v->wide = true;
+    v->elem_bytes = 1;
+    for (int i = 0; i < v->rank - 1; ++i) v->strides[i] /= 2;
+    v->dims[0] = static_cast<cuuint64_t>(K);
+    v->box[0] = static_cast<cuuint32_t>(kBoxK8);
+}
+
+inline bool matrix8_view(View* v, long long rows, int K, int box_rows) {
+    if (!matrix_view(v, rows, K, box_rows)) return false;
+    narrow(v, K);
+    return true;
+}
+
+// Weight rows in pair order (row_pairs_view): fc1 of either layout, or a plain [E, n, K].
+inline bool pairs8_view(View* v, int E, int n, int K, int box_pairs, bool fc1_chunked) {
+    const bool ok = fc1_chunked ? fc1_pairs_view(v, E, n / 2, K, box_pairs, true)
+                                : plain_pairs_view(v, E, n, K, box_pairs);
+    if (!ok) return false;
+    narrow(v, K);
+    return true;
+}
+
+// Weight rows in fragment order (quad_rows_view / fc1_quad_rows_chunked_view).
+inline bool quads8_view(View* v, int E, int n, int K, bool fc1_chunked) {
+    const bool ok = fc1_chunked ? fc1_quad_rows_chunked_view(v, E, n / 2, K) : quad_rows_view(v, E, n, K);
+    if (!ok) return false;
+    narrow(v, K);
+    return true;
+}
+
+inline bool matrix8(CUtensorMap* m, const void* p, long long rows, int K, int box_rows) {
+    View v;
+    return matrix8_view(&v, rows, K, box_rows) && encode(m, v, p);
+}
+
+inline bool pairs8(CUtensorMap* m, const void* w, int E, int n, int K, int box_pairs, bool fc1_chunked) {
+    View v;
+    return pairs8_view(&v, E, n, K, box_pairs, fc1_chunked) && encode(m, v, w);
+}
+
+inline bool quads8(CUtensorMap* m, const void* w, int E, int n, int K, bool fc1_chunked) {
+    View v;
+    return quads8_view(&v, E, n, K, fc1_chunked) && encode(m, v, w);
 }
 
 }  // namespace tmap
