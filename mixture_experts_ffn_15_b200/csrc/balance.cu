@@ -13,22 +13,25 @@
 // and counts for every sequence that its range meets, into slot b + s (walking along the
 // tokens either the block or the sequence advances, so slots are unique).  A second launch
 // adds each sequence's slots in order: no floating-point atomics, the same bits every time.
+// A batch that one block holds as one sequence is finished in the first launch.
+//
+// A row's E logits are spread over LPR lanes with 8 each (two 16-byte vectors where E is a
+// multiple of 4), 32 / LPR rows to a warp, the next rows' loads issued before the current
+// ones are used.  Bound by HBM: 4 T E bytes read, the gradient as much again and written.
+#include <type_traits>
+
 #include "common.cuh"
 #include "kernels.h"
 
 namespace moe {
 namespace {
 
-constexpr int kBThreads = 256;
+constexpr int kBThreads = 1024;
 constexpr int kBWarps = kBThreads / 32;
-constexpr int kPer = kMaxExperts / 32;   // logits a lane holds
+constexpr int kGThreads = 512;
+constexpr int kPer = 8;                  // logits a lane holds
 constexpr int kTokensPerBlockMin = 64;
-
-__device__ __forceinline__ float warp_max(float v) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-    return v;
-}
+constexpr int kOneBlockTokens = 256;     // up to here one block takes the batch
 
 // Sequence bounds with offsets clamped to [0, T] (nullptr: one sequence, the batch).
 __device__ __forceinline__ int seq_bound(const int32_t* seq, int s, int T) {
@@ -45,59 +48,143 @@ __device__ __forceinline__ int seq_at(const int32_t* seq, int S, int t, int T) {
     return lo;
 }
 
-// Softmax of one row, lane l holding logits l + 32 i.  fmaxf drops a NaN, but the
-// exponential of the NaN itself reaches the sum; a row of -inf alone gives zeros.
-__device__ __forceinline__ void row_softmax(const float* __restrict__ lg, int E, int lane, float* p) {
-    float m = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        const int e = lane + 32 * i;
-        p[i] = e < E ? lg[e] : -INFINITY;
-        m = fmaxf(m, p[i]);
+// The 8 logits of lane l (of LPR) of a row: with VEC, experts 4 l .. 4 l + 3 and
+// 4 LPR + 4 l .. + 3, else l + LPR i.
+template <int LPR, bool VEC>
+struct Row {
+    float v[kPer];
+    static __device__ __forceinline__ int expert(int l, int i) {
+        return VEC ? (i >> 2) * 4 * LPR + 4 * l + (i & 3) : l + LPR * i;
     }
-    m = warp_max(m);
-    const bool none = m == -INFINITY;
-    float sum = 0.f;
+    __device__ __forceinline__ void load(const float* __restrict__ row, int E, int l, bool live) {
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        p[i] = (none && p[i] == -INFINITY) ? 0.f : expf(p[i] - m);
-        sum += p[i];
+        for (int i = 0; i < kPer; ++i) v[i] = -INFINITY;
+        if (!live) return;
+        if constexpr (VEC) {
+#pragma unroll
+            for (int i = 0; i < kPer; i += 4)
+                if (expert(l, i) < E) {
+                    const float4 x = __ldg(reinterpret_cast<const float4*>(row + expert(l, i)));
+                    v[i] = x.x;
+                    v[i + 1] = x.y;
+                    v[i + 2] = x.z;
+                    v[i + 3] = x.w;
+                }
+        } else {
+#pragma unroll
+            for (int i = 0; i < kPer; ++i)
+                if (expert(l, i) < E) v[i] = __ldg(row + expert(l, i));
+        }
     }
-    sum = warp_sum(sum);
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    __device__ __forceinline__ void store(float* __restrict__ row, int E, int l) const {
+        if constexpr (VEC) {
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) p[i] *= inv;
+            for (int i = 0; i < kPer; i += 4)
+                if (expert(l, i) < E)
+                    *reinterpret_cast<float4*>(row + expert(l, i)) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < kPer; ++i)
+                if (expert(l, i) < E) row[expert(l, i)] = v[i];
+        }
+    }
+    // logits -> probabilities.  fmaxf drops a NaN, but the NaN's own exponential reaches the
+    // sum; a row of -inf alone gives zeros.
+    __device__ __forceinline__ void softmax() {
+        float m = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) m = fmaxf(m, v[i]);
+#pragma unroll
+        for (int o = LPR / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        // without a maximum: exp(-inf - 0) = 0 for a row of -inf, NaN for a NaN
+        const float base = m == -INFINITY ? 0.f : m;
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            v[i] = expf(v[i] - base);
+            sum += v[i];
+        }
+#pragma unroll
+        for (int o = LPR / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) v[i] *= inv;
+    }
+};
+
+struct BalanceParams {
+    const float* logits;
+    const int32_t* idx;
+    const uint8_t* mask;
+    const int32_t* seq;
+    int T, E, k, S, per_block, blocks;
+    float coef;
+    float* part_p;         // [blocks + S, E]
+    int32_t* part_c;       // [blocks + S, E]
+    int32_t* part_n;       // [blocks + S]
+    int32_t* ticket;
+    double* seq_loss;      // [S]
+    float* loss;
+    int32_t* counts;
+    float* probs;
+    int32_t* tokens;
+    int32_t* err;
+};
+
+// Sum of one double per thread, in a fixed order; the result on thread 0.
+__device__ __forceinline__ double block_sum(double v, double* s) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if (lane == 0) s[warp] = v;
+    __syncthreads();
+    if (warp == 0) {
+        v = lane < static_cast<int>(blockDim.x >> 5) ? s[lane] : 0.0;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    }
+    return v;
 }
 
-__global__ void __launch_bounds__(kBThreads)
-balance_partial_kernel(const float* __restrict__ logits, const int32_t* __restrict__ idx,
-                       const uint8_t* __restrict__ mask, const int32_t* __restrict__ seq, int T, int E,
-                       int k, int S, int per_block, float* __restrict__ part_p,
-                       int32_t* __restrict__ part_c, int32_t* __restrict__ part_n,
-                       int32_t* __restrict__ ticket, int32_t* __restrict__ err) {
+// Counts, mean probability and E f P of one expert of one sequence.
+__device__ __forceinline__ double finish_expert(const BalanceParams& p, int s, int e, double sum, long long c, int n) {
+    const double P = n > 0 ? sum / n : 0.0;
+    p.counts[static_cast<size_t>(s) * p.E + e] = static_cast<int32_t>(c);
+    p.probs[static_cast<size_t>(s) * p.E + e] = static_cast<float>(P);
+    return n > 0 ? static_cast<double>(c) / (static_cast<double>(n) * p.k) * P * p.E : 0.0;
+}
+
+template <int LPR, bool VEC>
+__global__ void __launch_bounds__(kBThreads, 1)
+balance_partial_kernel(const BalanceParams p) {
+    constexpr int kRows = 32 / LPR;     // rows of a warp
     __shared__ float s_p[kBWarps][kMaxExperts];
     __shared__ int s_c[kMaxExperts];
     __shared__ int s_n;
+    __shared__ double s_red[kBWarps];
     pdl_wait();
     pdl_trigger();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int b = blockIdx.x;
+    const int l = lane & (LPR - 1), sub = lane / LPR;
+    const int b = blockIdx.x, E = p.E, T = p.T, S = p.S;
     if (b == 0) {
-        if (threadIdx.x == 0) *ticket = 0;
-        if (seq && err) {
+        if (threadIdx.x == 0) *p.ticket = 0;
+        if (p.seq && p.err) {
             // reported, not trusted: every use below is clamped
-            bool bad = threadIdx.x == 0 && seq[0] != 0;
+            bool bad = threadIdx.x == 0 && p.seq[0] != 0;
             for (int s = threadIdx.x; s < S; s += kBThreads)
-                bad = bad || seq[s + 1] < seq[s] || seq[s + 1] > T;
-            if (bad) atomicOr(err, kErrBadExpert);
+                bad = bad || p.seq[s + 1] < p.seq[s] || p.seq[s + 1] > T;
+            if (bad) atomicOr(p.err, kErrBadExpert);
         }
     }
-    const int t0 = static_cast<int>(min(static_cast<long long>(b) * per_block, static_cast<long long>(T)));
-    const int t1 = static_cast<int>(min(static_cast<long long>(t0) + per_block, static_cast<long long>(T)));
-    for (int s = seq_at(seq, S, t0, T); s < S; ++s) {
-        const int a = max(seq_bound(seq, s, T), t0), z = min(seq_bound(seq, s + 1, T), t1);
-        if (seq_bound(seq, s, T) >= t1) break;
-        if (a >= z) continue;
+    const int t0 = static_cast<int>(min(static_cast<long long>(b) * p.per_block, static_cast<long long>(T)));
+    const int t1 = static_cast<int>(min(static_cast<long long>(t0) + p.per_block, static_cast<long long>(T)));
+    const bool single = p.blocks <= 1 && S == 1;   // one block finishes the batch
+    for (int s = seq_at(p.seq, S, t0, T); s < S; ++s) {
+        const int lo = seq_bound(p.seq, s, T);
+        if (lo >= t1 && !single) break;
+        const int a = max(lo, t0), z = min(seq_bound(p.seq, s + 1, T), t1);
+        if (a >= z && !single) continue;
         for (int e = threadIdx.x; e < E; e += kBThreads) s_c[e] = 0;
         if (threadIdx.x == 0) s_n = 0;
         __syncthreads();
@@ -105,138 +192,195 @@ balance_partial_kernel(const float* __restrict__ logits, const int32_t* __restri
 #pragma unroll
         for (int i = 0; i < kPer; ++i) acc[i] = 0.f;
         int n = 0;
-        for (int t = a + warp; t < z; t += kBWarps) {
-            if (mask && !mask[t]) continue;
-            ++n;
-            float p[kPer];
-            row_softmax(logits + static_cast<size_t>(t) * E, E, lane, p);
-#pragma unroll
-            for (int i = 0; i < kPer; ++i) acc[i] += p[i];
-            for (int j = lane; j < k; j += 32) {
-                const int e = idx[static_cast<size_t>(t) * k + j];
+        constexpr int kStep = kBWarps * kRows;
+        auto valid = [&](int t) { return t < z && (!p.mask || p.mask[t] != 0); };
+        auto row = [&](int t) { return p.logits + static_cast<size_t>(t) * E; };
+        int t = a + warp * kRows + sub;
+        bool live = valid(t);
+        Row<LPR, VEC> r, next;
+        r.load(row(t), E, l, live);
+        const int trips = (z - a - warp * kRows + kStep - 1) / kStep;   // of this warp
+        for (int it = 0; it < trips; ++it) {
+            const int tn = t + kStep;
+            const bool next_live = valid(tn);
+            next.load(row(tn), E, l, next_live);
+            for (int j = l; live && j < p.k; j += LPR) {
+                const int e = p.idx[static_cast<size_t>(t) * p.k + j];
                 if (static_cast<unsigned>(e) < static_cast<unsigned>(E)) atomicAdd(&s_c[e], 1);
-                else if (err) atomicOr(err, kErrBadExpert);
+                else if (p.err) atomicOr(p.err, kErrBadExpert);
             }
-        }
+            r.softmax();   // a row that takes no part holds -inf: zeros
 #pragma unroll
-        for (int i = 0; i < kPer; ++i)
-            if (lane + 32 * i < E) s_p[warp][lane + 32 * i] = acc[i];
-        if (lane == 0) atomicAdd(&s_n, n);
+            for (int i = 0; i < kPer; ++i) acc[i] += r.v[i];
+            n += live && l == 0;
+            t = tn;
+            live = next_live;
+            r = next;
+        }
+        // the warp's rows, then the warps, in order
+#pragma unroll
+        for (int o = LPR; o < 32; o <<= 1) {
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], o);
+        }
+        n = __reduce_add_sync(0xffffffffu, n);
+        if (sub == 0) {
+#pragma unroll
+            for (int i = 0; i < kPer; ++i)
+                if (Row<LPR, VEC>::expert(l, i) < E) s_p[warp][Row<LPR, VEC>::expert(l, i)] = acc[i];
+        }
+        if (lane == 0 && n) atomicAdd(&s_n, n);
         __syncthreads();
-        const size_t slot = static_cast<size_t>(b) + s;
-        for (int e = threadIdx.x; e < E; e += kBThreads) {
-            float v = 0.f;
+        const int e = threadIdx.x;
+        float v = 0.f;
+        if (e < E) {
 #pragma unroll
             for (int w = 0; w < kBWarps; ++w) v += s_p[w][e];
-            part_p[slot * E + e] = v;
-            part_c[slot * E + e] = s_c[e];
         }
-        if (threadIdx.x == 0) part_n[slot] = s_n;
+        if (single) {
+            // the whole batch is here
+            double term = 0.0;
+            if (e < E) term = finish_expert(p, 0, e, static_cast<double>(v), s_c[e], s_n);
+            term = block_sum(term, s_red);
+            if (threadIdx.x == 0) {
+                p.tokens[0] = s_n;
+                *p.loss = static_cast<float>(term * static_cast<double>(p.coef));
+            }
+            return;
+        }
+        const size_t slot = static_cast<size_t>(b) + s;
+        if (e < E) {
+            p.part_p[slot * E + e] = v;
+            p.part_c[slot * E + e] = s_c[e];
+        }
+        if (threadIdx.x == 0) p.part_n[slot] = s_n;
         __syncthreads();
     }
 }
 
-// One block per sequence adds its slots; the last block to finish adds the sequences.
+// One block per sequence adds its slots (strips of threads take every strip-th one, then
+// the strips in order); the last block to finish adds the sequences.
 __global__ void __launch_bounds__(kBThreads)
-balance_reduce_kernel(const float* __restrict__ part_p, const int32_t* __restrict__ part_c,
-                      const int32_t* __restrict__ part_n, const int32_t* __restrict__ seq, int T, int E,
-                      int k, int S, int per_block, float coef, int32_t* __restrict__ ticket,
-                      double* __restrict__ seq_loss, float* __restrict__ loss,
-                      int32_t* __restrict__ counts, float* __restrict__ probs,
-                      int32_t* __restrict__ tokens) {
+balance_reduce_kernel(const BalanceParams p) {
     __shared__ double s_sum[kBThreads];
-    __shared__ int s_last;
+    __shared__ int s_cnt[kBThreads];
+    __shared__ double s_red[kBWarps];
+    __shared__ int s_n, s_last;
+    if (threadIdx.x == 0) s_n = 0;
     pdl_wait();
     pdl_trigger();
-    const int s = blockIdx.x, e = threadIdx.x;
-    const int lo = seq_bound(seq, s, T), hi = seq_bound(seq, s + 1, T);
-    const int b0 = lo / per_block, b1 = hi > lo ? (hi - 1) / per_block + 1 : b0;
+    __syncthreads();
+    const int s = blockIdx.x, E = p.E;
+    const int strips = kBThreads / E, e = threadIdx.x % E, st = threadIdx.x / E;
+    const int lo = seq_bound(p.seq, s, p.T), hi = seq_bound(p.seq, s + 1, p.T);
+    const int b0 = lo / p.per_block, b1 = hi > lo ? (hi - 1) / p.per_block + 1 : b0;
     int n = 0;
-    for (int b = b0; b < b1; ++b) n += part_n[b + s];
-    double v = 0.0;
-    if (e < E) {
-        double sum = 0.0;
-        long long c = 0;
-        for (int b = b0; b < b1; ++b) {
-            sum += static_cast<double>(part_p[static_cast<size_t>(b + s) * E + e]);
-            c += part_c[static_cast<size_t>(b + s) * E + e];
+    for (int b = b0 + threadIdx.x; b < b1; b += kBThreads) n += p.part_n[b + s];
+    if (n) atomicAdd(&s_n, n);
+    double sum = 0.0;
+    int c = 0;
+    if (st < strips) {
+#pragma unroll 8
+        for (int b = b0 + st; b < b1; b += strips) {
+            sum += static_cast<double>(p.part_p[static_cast<size_t>(b + s) * E + e]);
+            c += p.part_c[static_cast<size_t>(b + s) * E + e];
         }
-        const double P = n > 0 ? sum / n : 0.0;
-        counts[static_cast<size_t>(s) * E + e] = static_cast<int32_t>(c);
-        probs[static_cast<size_t>(s) * E + e] = static_cast<float>(P);
-        if (n > 0) v = static_cast<double>(c) / (static_cast<double>(n) * k) * P * E;
     }
-    if (e == 0) tokens[s] = n;
-    s_sum[threadIdx.x] = v;
-    for (int d = kBThreads / 2; d > 0; d >>= 1) {
-        __syncthreads();
-        if (threadIdx.x < d) s_sum[threadIdx.x] += s_sum[threadIdx.x + d];
+    s_sum[threadIdx.x] = sum;
+    s_cnt[threadIdx.x] = c;
+    __syncthreads();
+    double v = 0.0;
+    if (st == 0) {
+        long long cc = c;
+        for (int i = 1; i < strips; ++i) {
+            sum += s_sum[i * E + e];
+            cc += s_cnt[i * E + e];
+        }
+        v = finish_expert(p, s, e, sum, cc, s_n);
+    }
+    if (threadIdx.x == 0) p.tokens[s] = s_n;
+    v = block_sum(v, s_red);
+    if (p.S == 1) {
+        if (threadIdx.x == 0) *p.loss = static_cast<float>(v * static_cast<double>(p.coef));
+        return;
     }
     if (threadIdx.x == 0) {
-        seq_loss[s] = s_sum[0];
+        p.seq_loss[s] = v;
         __threadfence();
-        s_last = atomicAdd(ticket, 1) == S - 1;
+        s_last = atomicAdd(p.ticket, 1) == p.S - 1;
     }
     __syncthreads();
     if (!s_last) return;
     __threadfence();
-    // the last block: sequences in a fixed order
     v = 0.0;
-    for (int i = threadIdx.x; i < S; i += kBThreads) v += __ldcg(seq_loss + i);
-    s_sum[threadIdx.x] = v;
-    for (int d = kBThreads / 2; d > 0; d >>= 1) {
-        __syncthreads();
-        if (threadIdx.x < d) s_sum[threadIdx.x] += s_sum[threadIdx.x + d];
-    }
-    if (threadIdx.x == 0) *loss = static_cast<float>(s_sum[0] * static_cast<double>(coef) / S);
+    for (int i = threadIdx.x; i < p.S; i += kBThreads) v += __ldcg(p.seq_loss + i);
+    v = block_sum(v, s_red);
+    if (threadIdx.x == 0) *p.loss = static_cast<float>(v * static_cast<double>(p.coef) / p.S);
 }
 
-__global__ void __launch_bounds__(kBThreads)
-balance_grad_kernel(const float* __restrict__ logits, const uint8_t* __restrict__ mask,
-                    const int32_t* __restrict__ seq, const int32_t* __restrict__ counts,
-                    const int32_t* __restrict__ tokens, int T, int E, int k, int S, float coef,
-                    const float* __restrict__ grad_loss, float* __restrict__ dlogits) {
+template <int LPR, bool VEC>
+__global__ void __launch_bounds__(kGThreads)
+balance_grad_kernel(const BalanceGradArgs a, int per_block) {
+    constexpr int kRows = 32 / LPR, kStep = (kGThreads / 32) * kRows;
     pdl_wait();
     pdl_trigger();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const float g = coef * (grad_loss ? *grad_loss : 1.f);
+    const int l = lane & (LPR - 1), sub = lane / LPR;
+    const int T = a.T, E = a.E;
+    const float g = a.coef * (a.grad_loss ? *a.grad_loss : 1.f);
+    const int t0 = static_cast<int>(min(static_cast<long long>(blockIdx.x) * per_block, static_cast<long long>(T)));
+    const int t1 = static_cast<int>(min(static_cast<long long>(t0) + per_block, static_cast<long long>(T)));
+    int t = t0 + warp * kRows + sub;
+    // the lane group's sequence: its bounds, shares less 1/E and scale; t only grows
+    int s = seq_at(a.seq_offsets, a.S, min(t, T - 1), T);
+    int lo = seq_bound(a.seq_offsets, s, T), hi = seq_bound(a.seq_offsets, s + 1, T);
     int have = -1;
     float f[kPer], scale = 0.f;
-    for (long long t = static_cast<long long>(blockIdx.x) * kBWarps + warp; t < T;
-         t += static_cast<long long>(gridDim.x) * kBWarps) {
-        float* d = dlogits + t * E;
-        const int s = seq_at(seq, S, static_cast<int>(t), T);
-        bool valid = t >= seq_bound(seq, s, T) && t < seq_bound(seq, s + 1, T);
-        if (valid && mask) valid = mask[t] != 0;
-        if (!valid) {
 #pragma unroll
-            for (int i = 0; i < kPer; ++i)
-                if (lane + 32 * i < E) d[lane + 32 * i] = 0.f;
-            continue;
+    for (int i = 0; i < kPer; ++i) f[i] = 0.f;
+    auto masked = [&](int u) { return u >= t1 || (a.mask && a.mask[u] == 0); };
+    auto row = [&](int u) { return a.logits + static_cast<size_t>(u) * E; };
+    bool off = masked(t);
+    Row<LPR, VEC> r, next;
+    r.load(row(t), E, l, !off);
+    const int trips = (t1 - t0 - warp * kRows + kStep - 1) / kStep;
+    for (int it = 0; it < trips; ++it) {
+        const int tn = t + kStep;
+        const bool next_off = masked(tn);
+        next.load(row(tn), E, l, !next_off);
+        while (t >= hi && s + 1 < a.S && t < t1) {
+            ++s;
+            lo = hi;
+            hi = seq_bound(a.seq_offsets, s + 1, T);
         }
-        if (s != have) {
+        const bool live = !off && t >= lo && t < hi;
+        if (live && s != have) {
             have = s;
-            const double n = tokens[s] > 0 ? static_cast<double>(tokens[s]) : 1.0;
-            scale = static_cast<float>(static_cast<double>(g) * E / (n * S));
+            const int n = a.tokens[s];
+            const double nd = n > 0 ? static_cast<double>(n) : 1.0;
+            scale = static_cast<float>(static_cast<double>(g) * E / (nd * a.S));
 #pragma unroll
             for (int i = 0; i < kPer; ++i) {
-                const int e = lane + 32 * i;
+                const int e = Row<LPR, VEC>::expert(l, i);
                 f[i] = 0.f;
                 if (e < E) {
-                    const long long c = counts[static_cast<size_t>(s) * E + e];
-                    f[i] = static_cast<float>(static_cast<double>(c * E - static_cast<long long>(tokens[s]) * k) /
-                                              (n * k * E));
+                    const long long c = a.counts[static_cast<size_t>(s) * E + e];
+                    f[i] = static_cast<float>(static_cast<double>(c * E - static_cast<long long>(n) * a.k) / (nd * a.k * E));
                 }
             }
         }
-        float p[kPer], dot = 0.f;
-        row_softmax(logits + t * E, E, lane, p);
+        r.softmax();
+        float dot = 0.f;
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) dot = fmaf(f[i], p[i], dot);
-        dot = warp_sum(dot);
+        for (int i = 0; i < kPer; ++i) dot = fmaf(f[i], r.v[i], dot);
 #pragma unroll
-        for (int i = 0; i < kPer; ++i)
-            if (lane + 32 * i < E) d[lane + 32 * i] = scale * (p[i] * (f[i] - dot));
+        for (int o = LPR / 2; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) r.v[i] = live ? scale * (r.v[i] * (f[i] - dot)) : 0.f;
+        if (t < t1) r.store(a.dlogits + static_cast<size_t>(t) * E, E, l);
+        t = tn;
+        off = next_off;
+        r = next;
     }
 }
 
@@ -249,9 +393,10 @@ struct BalanceLayout {
 
 BalanceLayout balance_layout(int T, int E, int S) {
     BalanceLayout L;
-    const int most = 2 * 148;
+    const int most = 148;
     L.per_block = (T + most - 1) / most;
     if (L.per_block < kTokensPerBlockMin) L.per_block = kTokensPerBlockMin;
+    if (T <= kOneBlockTokens) L.per_block = kOneBlockTokens;
     L.blocks = (T + L.per_block - 1) / L.per_block;
     const size_t slots = static_cast<size_t>(L.blocks) + S;
     L.ticket = 0;
@@ -263,6 +408,22 @@ BalanceLayout balance_layout(int T, int E, int S) {
     return L;
 }
 
+// fn(lanes per row, vector loads) with the smallest LPR that holds E logits at 8 a lane.
+template <typename F>
+cudaError_t by_experts(int E, F fn) {
+    const bool vec = E % 4 == 0;
+    auto go = [&](auto lpr) {
+        constexpr int L = decltype(lpr)::value;
+        return vec ? fn(lpr, std::true_type()) : fn(std::integral_constant<int, L>(), std::false_type());
+    };
+    if (E <= 8) return go(std::integral_constant<int, 1>());
+    if (E <= 16) return go(std::integral_constant<int, 2>());
+    if (E <= 32) return go(std::integral_constant<int, 4>());
+    if (E <= 64) return go(std::integral_constant<int, 8>());
+    if (E <= 128) return go(std::integral_constant<int, 16>());
+    return go(std::integral_constant<int, 32>());
+}
+
 }  // namespace
 
 size_t balance_workspace_bytes(int T, int E, int S) { return balance_layout(T, E, S).total; }
@@ -270,27 +431,27 @@ size_t balance_workspace_bytes(int T, int E, int S) { return balance_layout(T, E
 cudaError_t launch_balance_loss(const BalanceArgs& a, cudaStream_t s) {
     const BalanceLayout L = balance_layout(a.T, a.E, a.S);
     char* ws = static_cast<char*>(a.workspace);
-    int32_t* ticket = reinterpret_cast<int32_t*>(ws + L.ticket);
-    double* seq_loss = reinterpret_cast<double*>(ws + L.seq_loss);
-    int32_t* part_n = reinterpret_cast<int32_t*>(ws + L.part_n);
-    int32_t* part_c = reinterpret_cast<int32_t*>(ws + L.part_c);
-    float* part_p = reinterpret_cast<float*>(ws + L.part_p);
-    cudaError_t e = launch_k(balance_partial_kernel, dim3(L.blocks > 0 ? L.blocks : 1), dim3(kBThreads), 0, s,
-                             a.logits, a.topk_idx, a.mask, a.seq_offsets, a.T, a.E, a.k, a.S, L.per_block,
-                             part_p, part_c, part_n, ticket, a.err);
-    if (e != cudaSuccess) return e;
-    return launch_k(balance_reduce_kernel, dim3(a.S), dim3(kBThreads), 0, s,
-                    static_cast<const float*>(part_p), static_cast<const int32_t*>(part_c),
-                    static_cast<const int32_t*>(part_n), a.seq_offsets, a.T, a.E, a.k, a.S, L.per_block,
-                    a.coef, ticket, seq_loss, a.loss, a.counts, a.probs, a.tokens);
+    const BalanceParams p{a.logits, a.topk_idx, a.mask, a.seq_offsets, a.T, a.E, a.k, a.S, L.per_block, L.blocks,
+                          a.coef, reinterpret_cast<float*>(ws + L.part_p), reinterpret_cast<int32_t*>(ws + L.part_c),
+                          reinterpret_cast<int32_t*>(ws + L.part_n), reinterpret_cast<int32_t*>(ws + L.ticket),
+                          reinterpret_cast<double*>(ws + L.seq_loss), a.loss, a.counts, a.probs, a.tokens, a.err};
+    const dim3 grid(L.blocks > 0 ? L.blocks : 1), block(kBThreads);
+    const cudaError_t e = by_experts(a.E, [&](auto lpr, auto vec) {
+        return launch_k(balance_partial_kernel<decltype(lpr)::value, decltype(vec)::value>, grid, block, 0, s, p);
+    });
+    if (e != cudaSuccess || (L.blocks <= 1 && a.S == 1)) return e;
+    return launch_k(balance_reduce_kernel, dim3(a.S), block, 0, s, p);
 }
 
 cudaError_t launch_balance_grad(const BalanceGradArgs& a, cudaStream_t s) {
     if (a.T <= 0) return cudaSuccess;
-    const long long want = (a.T + kBWarps - 1) / kBWarps, most = static_cast<long long>(device_sm_count()) * 8;
-    return launch_k(balance_grad_kernel, dim3(static_cast<unsigned>(want < most ? want : most)),
-                    dim3(kBThreads), 0, s, a.logits, a.mask, a.seq_offsets, a.counts, a.tokens, a.T, a.E,
-                    a.k, a.S, a.coef, a.grad_loss, a.dlogits);
+    const int most = 2 * device_sm_count();
+    int per_block = (a.T + most - 1) / most;
+    if (per_block < 16) per_block = 16;
+    const dim3 grid((a.T + per_block - 1) / per_block), block(kGThreads);
+    return by_experts(a.E, [&](auto lpr, auto vec) {
+        return launch_k(balance_grad_kernel<decltype(lpr)::value, decltype(vec)::value>, grid, block, 0, s, a, per_block);
+    });
 }
 
 }  // namespace moe

@@ -186,9 +186,14 @@ def expert_ffn_q8(x_perm, offsets, fc1_q, fc1_scale, fc2_q, fc2_scale, y_perm=No
 
 
 def _same_device(t, *others):
+    dev = t.device
     for o in others:
-        if o is not None and o.device != t.device:
-            raise ValueError(f"every tensor must be on {t.device}, got one on {o.device}")
+        if o is not None and o.device != dev:
+            raise ValueError(f"every tensor must be on {dev}, got one on {o.device}")
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
 
 
 _HERE = contextlib.nullcontext()
@@ -222,8 +227,8 @@ def quantize_rows(x, q=None, scale=None, stream=None):
         _need(q, "q", torch.int8, (rows, K))
         _need(scale, "scale", torch.float32, (rows,))
         _same_device(x, q, scale)
-        check(_lib().moe_quantize_rows(_ptr(x), rows, K, _dtcode(x), _ptr(q), _ptr(scale),
-                                       _stream(s)), "moe_quantize_rows")
+        check(_lib().moe_quantize_rows(_addr(x), rows, K, _dtcode(x), _addr(q), _addr(scale),
+                                       s.cuda_stream), "moe_quantize_rows")
     return q, scale
 
 
@@ -258,9 +263,9 @@ def matmul_q8(a_q, a_scale, w_q, w_scale, offsets=None, bias=None, out=None,
         if bias is not None:
             _need(bias, "bias", out.dtype, lead)
         _same_device(a_q, a_scale, w_q, w_scale, offsets, bias, out, err_word)
-        check(_lib().moe_matmul_q8(_ptr(a_q), _ptr(a_scale), _ptr(w_q), _ptr(w_scale), _ptr(bias),
-                                   _ptr(offsets), rows, K, E, N, dt, _ptr(out), _ptr(err_word),
-                                   _stream(s)), "moe_matmul_q8")
+        check(_lib().moe_matmul_q8(_addr(a_q), _addr(a_scale), _addr(w_q), _addr(w_scale), _addr(bias),
+                                   _addr(offsets), rows, K, E, N, dt, _addr(out), _addr(err_word),
+                                   s.cuda_stream), "moe_matmul_q8")
     return out
 
 
@@ -295,11 +300,11 @@ def expert_ffn_w8a8(x_perm, offsets, fc1_q, fc1_scale, fc2_q, fc2_scale, y_perm=
         _need(workspace, "workspace", torch.uint8)
         _same_device(x_perm, offsets, fc1_q, fc1_scale, fc2_q, fc2_scale, fc1_bias, fc2_bias,
                      y_perm, workspace)
-        check(_lib().moe_expert_ffn_w8a8(_ptr(x_perm), _ptr(offsets), _ptr(fc1_q), _ptr(fc1_scale),
-                                         _ptr(fc2_q), _ptr(fc2_scale), _ptr(fc1_bias),
-                                         _ptr(fc2_bias), rows, H, E, I, _swiglu(*swiglu),
-                                         _layout(fc1_layout), _ptr(y_perm), _ptr(workspace),
-                                         workspace.numel(), _stream(s)), "moe_expert_ffn_w8a8")
+        check(_lib().moe_expert_ffn_w8a8(_addr(x_perm), _addr(offsets), _addr(fc1_q), _addr(fc1_scale),
+                                         _addr(fc2_q), _addr(fc2_scale), _addr(fc1_bias),
+                                         _addr(fc2_bias), rows, H, E, I, _swiglu(*swiglu),
+                                         _layout(fc1_layout), _addr(y_perm), _addr(workspace),
+                                         workspace.numel(), s.cuda_stream), "moe_expert_ffn_w8a8")
     return y_perm
 
 
@@ -337,12 +342,12 @@ def forward_w8a8(hidden, router_w, fc1_q, fc1_scale, fc2_q, fc2_scale, k, normal
         _need(workspace, "workspace", torch.uint8)
         _same_device(hidden, router_w, router_bias, fc1_q, fc1_scale, fc2_q, fc2_scale, fc1_bias,
                      fc2_bias, norm_weight, out, workspace)
-        check(_lib().moe_forward_w8a8(_ptr(hidden), _ptr(norm_weight), float(norm_eps),
-                                      _ptr(router_w), _ptr(router_bias), _ptr(fc1_q),
-                                      _ptr(fc1_scale), _ptr(fc2_q), _ptr(fc2_scale), _ptr(fc1_bias),
-                                      _ptr(fc2_bias), T, H, E, k, I, int(bool(normalize)),
-                                      _swiglu(*swiglu), _layout(fc1_layout), _ptr(out),
-                                      _ptr(workspace), workspace.numel(), _stream(s)),
+        check(_lib().moe_forward_w8a8(_addr(hidden), _addr(norm_weight), float(norm_eps),
+                                      _addr(router_w), _addr(router_bias), _addr(fc1_q),
+                                      _addr(fc1_scale), _addr(fc2_q), _addr(fc2_scale), _addr(fc1_bias),
+                                      _addr(fc2_bias), T, H, E, k, I, int(bool(normalize)),
+                                      _swiglu(*swiglu), _layout(fc1_layout), _addr(out),
+                                      _addr(workspace), workspace.numel(), s.cuda_stream),
               "moe_forward_w8a8")
     return out
 
@@ -388,10 +393,10 @@ def balance_loss(logits, topk_idx, coef=1.0, mask=None, seq_offsets=None, err_wo
                                     dtype=torch.uint8, device=dev)
         _need(workspace, "workspace", torch.uint8)
         _same_device(logits, topk_idx, mask, seq_offsets, err_word, workspace)
-        check(_lib().moe_balance_loss(_ptr(logits), _ptr(topk_idx), _ptr(mask), _ptr(seq_offsets),
-                                      T, E, topk_idx.shape[1], S, float(coef), _ptr(loss),
-                                      _ptr(counts), _ptr(probs), _ptr(tokens), _ptr(err_word),
-                                      _ptr(workspace), workspace.numel(), _stream(s)),
+        check(_lib().moe_balance_loss(_addr(logits), _addr(topk_idx), _addr(mask), _addr(seq_offsets),
+                                      T, E, topk_idx.shape[1], S, float(coef), _addr(loss),
+                                      _addr(counts), _addr(probs), _addr(tokens), _addr(err_word),
+                                      _addr(workspace), workspace.numel(), s.cuda_stream),
               "moe_balance_loss")
     return dict(loss=loss, counts=counts, probs=probs, tokens=tokens)
 
@@ -415,10 +420,10 @@ def balance_loss_backward(logits, k, counts, tokens, coef=1.0, mask=None, seq_of
             dlogits = torch.empty_like(logits)
         _need(dlogits, "dlogits", torch.float32, (T, E))
         _same_device(logits, counts, tokens, mask, seq_offsets, grad_loss, dlogits)
-        check(_lib().moe_balance_loss_backward(_ptr(logits), _ptr(mask), _ptr(seq_offsets),
-                                               _ptr(counts), _ptr(tokens), T, E, int(k), S,
-                                               float(coef), _ptr(grad_loss), _ptr(dlogits),
-                                               _stream(s)), "moe_balance_loss_backward")
+        check(_lib().moe_balance_loss_backward(_addr(logits), _addr(mask), _addr(seq_offsets),
+                                               _addr(counts), _addr(tokens), T, E, int(k), S,
+                                               float(coef), _addr(grad_loss), _addr(dlogits),
+                                               s.cuda_stream), "moe_balance_loss_backward")
     return dlogits
 
 

@@ -4,7 +4,8 @@ Bounds: a float32 softmax probability is within 24 U32 + 2 |logit - max| U32 of 
 value (the difference rounds once, the exponential is within 2 ulp, the sum of E terms by a
 tree of depth 5 on up to 8 terms a lane rounds 13 times, the quotient and the product once
 each), with U32 = 2^-24; logits here stay within 20 of their row's maximum: 64 U32 relative.
-P adds partial float32 sums of at most 56 such terms a warp and 8 warps: another 64 U32.
+P adds float32 sums of at most 27 such terms a lane, over 5 shuffles and 32 warps: another
+64 U32 (the blocks' sums are added in float64).
 The loss is a sum of non-negative terms f P: the same relative bound, and its own rounding.
 The gradient coef E / (S n) p (f - sum f p), with f less 1/E: |d| <= 64 U32 p |f - dot| from
 p, and (64 + 16) U32 sum p |f| from the dot product; f, the scale and the products a few U32
@@ -88,10 +89,18 @@ def test_sequences_that_are_empty_short_and_leave_a_tail():
     T, E, k = 500, 32, 2
     lg = rng.standard_normal((T, E)).astype(np.float32).astype(np.float64)
     idx = np.argsort(-lg, axis=1, kind="stable")[:, :k]
-    for seq in ([0, 0, 1, 1, 3, 300, 300, 450], [0, 0, 0], [0, 500, 500], [0, 64, 128, 129, 500]):
+    for seq in ([0, 0, 1, 1, 3, 300, 300, 450], [0, 0, 0], [0, 500, 500], [0, 64, 128, 129, 500], [0, 0], [0, 7]):
         mask = rng.random(T) < 0.7
         mask[1:3] = False          # a whole sequence masked in the first list
         compare(run(lg, idx, 1.5, mask, seq), lg, idx, 1.5, mask, seq)
+
+
+def test_one_short_sequence_in_a_small_batch():
+    rng = np.random.default_rng(8)
+    lg = rng.standard_normal((20, 16)).astype(np.float32).astype(np.float64)
+    idx = np.argsort(-lg, axis=1, kind="stable")[:, :2]
+    for seq in ([0, 0], [0, 3], [0, 20], [0, 0, 20], [0, 20, 20]):
+        compare(run(lg, idx, 1.0, seq=seq), lg, idx, 1.0, None, seq)
 
 
 def test_no_tokens_at_all():
