@@ -127,20 +127,26 @@ bool valid_w8a8_ffn(int H, int I) {
     return H > 0 && I > 0 && H % 32 == 0 && I % 32 == 0 && H <= kQ8MaxK && I <= kQ8MaxK;
 }
 
-// Workspace of the int8 expert FFN: error word, the int8 rows and scales of x_perm, the
-// float32 activations, their int8 rows and scales.
+// Workspace of the int8 expert FFN: what must start at zero (error word, the token tiles'
+// counters, the activation rows' maxima), the int8 rows and scales of x_perm and of the
+// activations, and the float32 activations where one launch does not cut them to 8 bits.
 struct W8a8Layout {
-    size_t err, xq, xs, act, aq, as, total;
+    size_t err, arrived, amax, clear_end, xq, xs, act, aq, as, total;
+    bool act8;
 };
 
-W8a8Layout w8a8_layout(int rows, int H, int I) {
+W8a8Layout w8a8_layout(int rows, int H, int E, int I) {
     const size_t r = static_cast<size_t>(rows);
     Carver c;
     W8a8Layout L;
+    L.act8 = q8_act8_supported(rows, E, I);
     L.err = c.take(kAlign);
+    L.arrived = c.take(L.act8 ? static_cast<size_t>(q8_act8_tiles(rows, E)) * 4 : 0);
+    L.amax = c.take(L.act8 ? r * 4 : 0);
+    L.clear_end = c.off;
     L.xq = c.take(r * H);
     L.xs = c.take(r * 4);
-    L.act = c.take(r * I * 4);
+    L.act = c.take(L.act8 ? 0 : r * I * 4);
     L.aq = c.take(r * I);
     L.as = c.take(r * 4);
     L.total = c.off;
@@ -170,7 +176,7 @@ W8a8FwdLayout w8a8_fwd_layout(int T, int H, int E, int k, int I) {
     L.x_perm = c.take(rows * H * 2);
     L.y = c.take(rows * H * 2);
     L.xn = c.take(t * H * 2);   // the normalised input (pre-FFN norm)
-    L.ffn = c.take(w8a8_layout(static_cast<int>(rows), H, I).total);
+    L.ffn = c.take(w8a8_layout(static_cast<int>(rows), H, E, I).total);
     L.total = c.off;
     return L;
 }
@@ -773,10 +779,11 @@ moe_status moe_matmul_q8(const int8_t* a_q, const float* a_scale, const int8_t* 
 
 size_t moe_expert_ffn_w8a8_workspace_size(int rows, int H, int E, int I) {
     if (rows < 0 || E <= 0 || E > kMaxExperts || !valid_w8a8_ffn(H, I)) return 0;
-    return w8a8_layout(rows, H, I).total;
+    return w8a8_layout(rows, H, E, I).total;
 }
 
-// The int8 expert FFN of valid arguments; err is cleared by the caller.
+// The int8 expert FFN of valid arguments.  Clears the start of its workspace; `err` may be
+// another word, cleared by the caller.
 static moe_status w8a8_ffn(const void* x_perm, const int32_t* offsets, const int8_t* fc1_q,
                            const float* fc1_scale, const int8_t* fc2_q, const float* fc2_scale, int rows,
                            int H, int E, int I, const FfnAttrs& ep, void* y_perm, char* ws,
@@ -786,6 +793,7 @@ static moe_status w8a8_ffn(const void* x_perm, const int32_t* offsets, const int
     float* act = reinterpret_cast<float*>(ws + L.act);
     int8_t* aq = reinterpret_cast<int8_t*>(ws + L.aq);
     float* as = reinterpret_cast<float*>(ws + L.as);
+    MOE_CUDA(launch_clear(ws + L.err, L.clear_end - L.err, s));
     MOE_CUDA(launch_quantize_rows(x_perm, rows, H, true, xq, xs, s));
     Q8GemmArgs g;
     g.a_q = xq;
@@ -801,11 +809,20 @@ static moe_status w8a8_ffn(const void* x_perm, const int32_t* offsets, const int
     g.swiglu = true;
     g.act = ep.act;
     g.fc1_chunked = ep.fc1_chunked;
-    g.out = act;
     g.err = err;
-    MOE_CUDA(launch_q8_gemm(g, s));
-    if (mid) record_event(mid, s);
-    MOE_CUDA(launch_quantize_rows(act, rows, I, false, aq, as, s));
+    if (L.act8) {
+        g.out = aq;
+        g.act8_scale = as;
+        g.act8_amax = reinterpret_cast<uint32_t*>(ws + L.amax);
+        g.act8_arrived = reinterpret_cast<int32_t*>(ws + L.arrived);
+        MOE_CUDA(launch_q8_gemm(g, s));
+        if (mid) record_event(mid, s);
+    } else {
+        g.out = act;
+        MOE_CUDA(launch_q8_gemm(g, s));
+        if (mid) record_event(mid, s);
+        MOE_CUDA(launch_quantize_rows(act, rows, I, false, aq, as, s));
+    }
     g = Q8GemmArgs();
     g.a_q = aq;
     g.a_scale = as;
@@ -839,12 +856,11 @@ moe_status moe_expert_ffn_w8a8(const void* x_perm, const int32_t* offsets, const
         !aligned(workspace, kAlign) || (fc1_bias && !aligned(fc1_bias, 2)) ||
         (fc2_bias && !aligned(fc2_bias, 2)))
         return MOE_ERR_INVALID_ARG;
-    const W8a8Layout L = w8a8_layout(rows, H, I);
+    const W8a8Layout L = w8a8_layout(rows, H, E, I);
     if (ws_bytes < L.total) return MOE_ERR_INVALID_ARG;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     char* ws = static_cast<char*>(workspace);
     int32_t* err = reinterpret_cast<int32_t*>(ws + L.err);
-    MOE_CUDA(launch_clear(err, kAlign, s));
     return w8a8_ffn(x_perm, offsets, fc1_q, fc1_scale, fc2_q, fc2_scale, rows, H, E, I,
                     make_ffn_attrs(act, fc1_layout, fc1_bias, fc2_bias), y_perm, ws, L, err, s, nullptr);
 }
@@ -899,7 +915,7 @@ moe_status moe_forward_w8a8(const void* hidden, const void* norm_weight, float n
     record(2, s);
     st = w8a8_ffn(ws + L.x_perm, rb.offsets, fc1_q, fc1_scale, fc2_q, fc2_scale, rows, H, E, I,
                   make_ffn_attrs(act, fc1_layout, fc1_bias, fc2_bias), ws + L.y, ws + L.ffn,
-                  w8a8_layout(rows, H, I), i32(0), s, g_events_on ? g_events[3] : nullptr);
+                  w8a8_layout(rows, H, E, I), i32(0), s, g_events_on ? g_events[3] : nullptr);
     if (st != MOE_OK) return st;
     record(4, s);
     MOE_CUDA(launch_combine(ws + L.y, rb.perm_dst, rb.w, T, H, k, true, out, s));

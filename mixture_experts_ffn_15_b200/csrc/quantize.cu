@@ -49,12 +49,18 @@ struct Vec8 {
     }
     // bits of the largest |element|, as float32 (a NaN is larger than an infinity)
     __device__ __forceinline__ uint32_t amax() const {
-        float f[8];
-        get(f);
-        uint32_t m = 0;
+        if constexpr (BF16) {
+            // two 16-bit magnitudes at a time
+            const uint32_t m = __vmaxu2(__vmaxu2(a.x & 0x7fff7fffu, a.y & 0x7fff7fffu),
+                                        __vmaxu2(a.z & 0x7fff7fffu, a.w & 0x7fff7fffu));
+            return max(m & 0xffff0000u, m << 16);
+        } else {
+            const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+            uint32_t m = 0;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(f[i]) & 0x7fffffffu);
-        return m;
+            for (int i = 0; i < 8; ++i) m = max(m, w[i] & 0x7fffffffu);
+            return m;
+        }
     }
 };
 

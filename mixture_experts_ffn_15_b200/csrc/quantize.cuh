@@ -53,25 +53,26 @@ __device__ __forceinline__ int round_near_half(float x, float v, float amax) {
 // N values -> N whole numbers (in the low bytes of n).
 template <bool BF16, int N>
 __device__ __forceinline__ void quantize_n(const float* f, const RowQuant& r, uint32_t* n) {
-    // v + 1.5 * 2^23 leaves round-to-nearest-even of v in the low bits (two's complement)
+    // x inv + 1.5 * 2^23, rounded once, holds the nearest whole number of x inv in its low
+    // bits (two's complement)
     constexpr float kMagic = 12582912.f;
-    uint32_t near = 0;
+    bool near = false;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        const float v = f[i] * r.pre * r.inv;
-        const float t = v + kMagic;
+        const float x = f[i] * r.pre;
+        const float t = fmaf(x, r.inv, kMagic);
         n[i] = __float_as_uint(t);
-        if (fabsf(v - (t - kMagic)) > 0.4999f) near |= 1u << i;
+        near = near || fabsf(fmaf(x, r.inv, kMagic - t)) > 0.4999f;
     }
     if (near) {
 #pragma unroll
-        for (int i = 0; i < N; ++i)
-            if (near & (1u << i)) {
-                const float x = f[i] * r.pre;
+        for (int i = 0; i < N; ++i) {
+            const float x = f[i] * r.pre;
+            if (fabsf(fmaf(x, r.inv, kMagic - __uint_as_float(n[i]))) > 0.4999f)
                 n[i] = static_cast<uint32_t>(round_near_half<BF16>(x, x * r.inv, r.amax));
-            }
+        }
     }
-    if (r.inv == 0.f) {
+    if (r.inv == 0.f) {   // an infinity or a NaN times 0 is no whole number
 #pragma unroll
         for (int i = 0; i < N; ++i) n[i] = 0;
     }

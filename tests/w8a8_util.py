@@ -10,9 +10,10 @@ factor 1.01 covers the second-order terms.
 FFN: the gate and up values carry the product's error (no output rounding).  act =
 g sigmoid(alpha g) (u + beta): |d act / d g| <= 1.1 |u + beta| (the derivative of silu is at
 most 1.1, scaling alpha does not change it), |d act / d u| = |g sigmoid(alpha g)|; the
-exponential is within 2 ulp of a float32 exponential of its rounded argument (|alpha g| U32
-absolute in the exponent), and the sum, quotient, sum and product add an ulp each: 16 U32 +
-2 |alpha g| U32 of |act| in all (an ulp is 2 U32).  The int8 activation of an element can
+exponential's argument alpha g, its product with log2 e and log2 e itself round (|alpha g| U32
+each at most, absolute in the exponent), the exponential and the quotient are within 2 ulp and
+the two sums and two products add half an ulp each: (12 + 3 |alpha g|) U32 of |act| in all (an
+ulp is at most 2 U32), 16 U32 taken for the first.  The int8 activation of an element can
 therefore differ by one step where its quotient v = 127 a / amax lies within
 delta = 127 (err_i + |a_i| / amax max err) / amax of a half, and the row's scale by
 max err / amax of itself."""
@@ -55,7 +56,7 @@ def ffn_with_bound(x, q1, s1, q2, s2, layout, act, b1=None, b2=None):
     gc, uc = np.minimum(g, limit), np.clip(u, -limit, limit)
     sg = np.abs(O.swiglu(g, np.ones_like(u), alpha, 0.0, limit)) if beta == 0.0 else \
         np.abs(gc / (1 + np.exp(-alpha * gc)))
-    ea = 1.1 * np.abs(uc + beta) * eg + sg * eu + (16 + 2 * np.abs(alpha * gc)) * U32 * np.abs(a)
+    ea = 1.1 * np.abs(uc + beta) * eg + sg * eu + (16 + 3 * np.abs(alpha * gc)) * U32 * np.abs(a)
     aq, as_ = O.quantize_rows(a)
     amax = np.max(np.abs(a), axis=1, keepdims=True)
     safe = np.where(amax > 0, amax, 1.0)
