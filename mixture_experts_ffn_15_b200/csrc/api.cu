@@ -127,26 +127,20 @@ bool valid_w8a8_ffn(int H, int I) {
     return H > 0 && I > 0 && H % 32 == 0 && I % 32 == 0 && H <= kQ8MaxK && I <= kQ8MaxK;
 }
 
-// Workspace of the int8 expert FFN: what must start at zero (error word, the token tiles'
-// counters, the activation rows' maxima), the int8 rows and scales of x_perm and of the
-// activations, and the float32 activations where one launch does not cut them to 8 bits.
+// Workspace of the int8 expert FFN: error word, the int8 rows and scales of x_perm, the
+// float32 activations, their int8 rows and scales.
 struct W8a8Layout {
-    size_t err, arrived, amax, clear_end, xq, xs, act, aq, as, total;
-    bool act8;
+    size_t err, xq, xs, act, aq, as, total;
 };
 
 W8a8Layout w8a8_layout(int rows, int H, int E, int I) {
     const size_t r = static_cast<size_t>(rows);
     Carver c;
     W8a8Layout L;
-    L.act8 = q8_act8_supported(rows, E, I);
     L.err = c.take(kAlign);
-    L.arrived = c.take(L.act8 ? static_cast<size_t>(q8_act8_tiles(rows, E)) * 4 : 0);
-    L.amax = c.take(L.act8 ? r * 4 : 0);
-    L.clear_end = c.off;
     L.xq = c.take(r * H);
     L.xs = c.take(r * 4);
-    L.act = c.take(L.act8 ? 0 : r * I * 4);
+    L.act = c.take(r * I * 4);
     L.aq = c.take(r * I);
     L.as = c.take(r * 4);
     L.total = c.off;
@@ -793,7 +787,7 @@ static moe_status w8a8_ffn(const void* x_perm, const int32_t* offsets, const int
     float* act = reinterpret_cast<float*>(ws + L.act);
     int8_t* aq = reinterpret_cast<int8_t*>(ws + L.aq);
     float* as = reinterpret_cast<float*>(ws + L.as);
-    MOE_CUDA(launch_clear(ws + L.err, L.clear_end - L.err, s));
+    MOE_CUDA(launch_clear(ws + L.err, kAlign, s));
     MOE_CUDA(launch_quantize_rows(x_perm, rows, H, true, xq, xs, s));
     Q8GemmArgs g;
     g.a_q = xq;
@@ -810,19 +804,10 @@ static moe_status w8a8_ffn(const void* x_perm, const int32_t* offsets, const int
     g.act = ep.act;
     g.fc1_chunked = ep.fc1_chunked;
     g.err = err;
-    if (L.act8) {
-        g.out = aq;
-        g.act8_scale = as;
-        g.act8_amax = reinterpret_cast<uint32_t*>(ws + L.amax);
-        g.act8_arrived = reinterpret_cast<int32_t*>(ws + L.arrived);
-        MOE_CUDA(launch_q8_gemm(g, s));
-        if (mid) record_event(mid, s);
-    } else {
-        g.out = act;
-        MOE_CUDA(launch_q8_gemm(g, s));
-        if (mid) record_event(mid, s);
-        MOE_CUDA(launch_quantize_rows(act, rows, I, false, aq, as, s));
-    }
+    g.out = act;
+    MOE_CUDA(launch_q8_gemm(g, s));
+    if (mid) record_event(mid, s);
+    MOE_CUDA(launch_quantize_rows(act, rows, I, false, aq, as, s));
     g = Q8GemmArgs();
     g.a_q = aq;
     g.a_scale = as;

@@ -17,7 +17,6 @@
 
 #include "common.cuh"
 #include "kernels.h"
-#include "quantize.cuh"
 #include "sm100.cuh"
 #include "tile_map.cuh"
 #include "tmap.cuh"
@@ -30,10 +29,7 @@ using namespace sm100;
 constexpr int kBK = tmap::kBoxK8;    // K per ring slot: one 128-byte row
 constexpr uint64_t kWaitNs = 2000000000ull;
 
-// OUT_SWIGLU: float32 activations.  OUT_ACT8 (pair kernel): activations cut to 8 bits in the
-// same launch.
-enum OutMode : int { OUT_F32 = 0, OUT_BF16 = 1, OUT_SWIGLU = 2, OUT_ACT8 = 3 };
-__host__ __device__ constexpr bool is_swiglu(int mode) { return mode == OUT_SWIGLU || mode == OUT_ACT8; }
+enum OutMode : int { OUT_F32 = 0, OUT_BF16 = 1, OUT_SWIGLU = 2 };
 
 struct Q8Params {
     const int32_t* offsets;   // [E+1] device, or nullptr: one group of `rows` rows
@@ -45,16 +41,12 @@ struct Q8Params {
     int32_t* err;
     SwigluAttr act;
     bool chunked;             // SwiGLU: scales and bias in the chunked layout
-    // OUT_ACT8: out [rows, N / 2] int8
-    float* out_scale;         // [rows]
-    uint32_t* amax;           // [rows] bits of max |activation|, zero on entry
-    int32_t* arrived;         // one counter per token tile, zero on entry
 };
 
 // Scale and bias of weight row wr (SwiGLU: in interleaved order) of expert g.
 template <int MODE>
 __device__ __forceinline__ void channel(const Q8Params& p, int g, int wr, float* scale, float* bias) {
-    const int row = is_swiglu(MODE) ? fc1_row(wr, p.N / 2, p.chunked) : wr;
+    const int row = MODE == OUT_SWIGLU ? fc1_row(wr, p.N / 2, p.chunked) : wr;
     const size_t i = static_cast<size_t>(g) * p.N + row;
     *scale = p.sw[i];
     *bias = 0.f;
@@ -320,8 +312,9 @@ q8_stream_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
 // columns).  The weight rows are loaded in fragment order (lane 8 q + j of a 32-lane
 // quadrant holds the quadrant's row 4 j + q), so that a 16x256b accumulator fragment gives a
 // thread four consecutive weight rows of two tokens, stored straight from registers.
-// Ten warps a CTA: 0 the TMA producer, 1 the MMA issuer (even CTA), 2-9 the epilogue.
-constexpr int kPThreads = 320;
+// A CTA's warps: 0 the TMA producer, 1 the MMA issuer (even CTA), then the epilogue.
+constexpr int kPEpi = 8;
+constexpr int kPThreads = 64 + 32 * kPEpi;
 constexpr int kPWRows = 128;
 constexpr int kPTok = 256;
 constexpr int kPSlots = 6;
@@ -348,29 +341,6 @@ __device__ __forceinline__ PUnit pair_unit(long long u, int MT, int G, const int
     d.nrows = min(kPTok, s_off[d.g + 1] - d.row0);
     d.n = ((d.nrows + 31) / 32) * 32;   // each CTA's half: a multiple of 16 rows
     return d;
-}
-
-__device__ __forceinline__ int ld_acquire(const int32_t* p) {
-    int v;
-    asm volatile("ld.acquire.gpu.global.b32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
-    return v;
-}
-
-// Bounded wait for *ctr >= target (every lane of the warp returns the same).
-__device__ __forceinline__ bool wait_count(const int32_t* ctr, int target, volatile int* abort, int lane) {
-    bool ok = true;
-    if (lane == 0) {
-        const uint64_t t0 = global_timer_ns();
-        while (ld_acquire(ctr) < target) {
-            if (*abort || global_timer_ns() - t0 > kWaitNs) {
-                *abort = 1;
-                ok = false;
-                break;
-            }
-            __nanosleep(32);
-        }
-    }
-    return __shfl_sync(0xffffffffu, ok, 0);
 }
 
 template <int MODE>
@@ -402,7 +372,7 @@ q8_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
         }
         for (int a = 0; a < 2; ++a) {
             mbar_init(smem_u32(&tfull[a]), 1);
-            mbar_init(smem_u32(&tempty[a]), 16); // 8 epilogue warps x 2 CTAs
+            mbar_init(smem_u32(&tempty[a]), 2 * kPEpi);   // both CTAs'
         }
         *abort_flag = 0;
         fence_mbar_init();
@@ -428,9 +398,6 @@ q8_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
     const int MT = (p.N + 2 * kPWRows - 1) / (2 * kPWRows);
     const long long units = static_cast<long long>(s_pre[G]) * MT;
     const int pair = static_cast<int>(blockIdx.x >> 1), npairs = static_cast<int>(gridDim.x >> 1);
-    // units strided over the pairs.  OUT_ACT8: the grid is a multiple of MT pairs, so that MT
-    // neighbouring pairs always work on one token tile together: a tile whose units fell into
-    // two rounds of the grid would hold up pairs of the first for the second.
     const int nk = (p.K + kBK - 1) / kBK;
 
     if (warp == 0) {
@@ -443,7 +410,7 @@ q8_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
             // weight views: plain (k, j, q, Q, e) at (k, 0, 0, w_in / 32, g); chunked fc1
             // (k, j, s, qq, X) at (k, 0, 0, 0, g I / 8 + w_in / 32)
             const int w_in = d.mt * 2 * kPWRows + static_cast<int>(rank) * kPWRows;
-            const bool chunked = is_swiglu(MODE) && p.chunked;
+            const bool chunked = MODE == OUT_SWIGLU && p.chunked;
             const int wc3 = chunked ? 0 : w_in / 32;
             const int wc4 = chunked ? d.g * (p.N / 16) + w_in / 32 : d.g;
             const uint32_t bytes = static_cast<uint32_t>(2 * (kPABytes + kPBBytes));
@@ -516,6 +483,7 @@ q8_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
         // 4 fj .. 4 fj + 3 of its quadrant for tokens 8 m + 2 ft + e of a 32-token chunk.
         const int quad = warp & 3;
         const int part = (warp - 2) >> 2;
+        constexpr int kParts = kPEpi / 4;
         const int fj = lane >> 2, ft = lane & 3;
         int acc = 0;
         uint32_t acc_phase = 0;
@@ -533,99 +501,8 @@ q8_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
             tc_fence_after();
             const uint32_t tb = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) +
                                 static_cast<uint32_t>(acc * kPAccCols);
-            if constexpr (MODE == OUT_ACT8) {
-                // (1) activations into registers, and the largest of every token's into amax
-                float a[4][16];   // [chunk][2 * (2 m + e) + (output 0, 1)]
-#pragma unroll
-                for (int ci = 0; ci < 4; ++ci) {
-                    const int c = part * 32 + ci * 64;
-                    if (c >= d.nrows) break;
-                    uint32_t lo[16], hi[16];
-                    tmem_ld_16x256b_x4(tb + c, lo);
-                    tmem_ld_16x256b_x4(tb + (16u << 16) + c, hi);
-                    float sa[8];
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        sa[j] = __ldg(p.sa + d.row0 + min(c + 8 * (j >> 1) + 2 * ft + (j & 1), d.nrows - 1));
-                    tmem_wait_ld();
-                    uint32_t m[8];
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const int i0 = 4 * (j >> 1) + (j & 1);
-                        const float g0 = fmaf(static_cast<float>(static_cast<int>(lo[i0])), sa[j] * sw[0], bias[0]);
-                        const float u0 = fmaf(static_cast<float>(static_cast<int>(lo[i0 + 2])), sa[j] * sw[1], bias[1]);
-                        const float g1 = fmaf(static_cast<float>(static_cast<int>(hi[i0])), sa[j] * sw[2], bias[2]);
-                        const float u1 = fmaf(static_cast<float>(static_cast<int>(hi[i0 + 2])), sa[j] * sw[3], bias[3]);
-                        a[ci][2 * j] = swiglu_attr_fast(g0, u0, p.act);
-                        a[ci][2 * j + 1] = swiglu_attr_fast(g1, u1, p.act);
-                        m[j] = max(__float_as_uint(a[ci][2 * j]) & 0x7fffffffu,
-                                   __float_as_uint(a[ci][2 * j + 1]) & 0x7fffffffu);
-                    }
-                    // over the warp's 16 outputs (lanes of equal ft), each step halving the
-                    // tokens a lane keeps: lane (fj, ft) ends with token j = fj's bits reversed
-#pragma unroll
-                    for (int h = 4; h > 0; h >>= 1) {
-                        const bool upper = (lane & (4 * h)) != 0;
-#pragma unroll
-                        for (int j = 0; j < h; ++j) {
-                            const uint32_t got = __shfl_xor_sync(0xffffffffu, upper ? m[j] : m[j + h], 4 * h);
-                            m[j] = max(upper ? m[j + h] : m[j], got);
-                        }
-                    }
-                    const int j = fj;   // bits: 16 -> 4, 8 -> 2, 4 -> 1
-                    const int tok = c + 8 * (j >> 1) + 2 * ft + (j & 1);
-                    if (wvalid && tok < d.nrows) atomicMax(p.amax + d.row0 + tok, m[0]);
-                }
-                // the accumulator is free; the tile's maxima are complete once all 16 warps of
-                // each of its MT units have been here
-                tc_fence_before();
-                __threadfence();
-                __syncwarp();
-                const int tile = static_cast<int>(u / MT);
-                if (lane == 0) {
-                    mbar_arrive_cluster(mapa_shared(smem_u32(&tempty[acc]), 0));
-                    atomicAdd(p.arrived + tile, 1);
-                }
-                acc ^= 1;
-                if (acc == 0) acc_phase ^= 1u;
-                if (!wait_count(p.arrived + tile, 16 * MT, abort_flag, lane)) break;
-                // (2) whole numbers; neighbouring lanes (fj, fj ^ 1) swap one token of each
-                // pair, so that a store is 4 outputs of one token
-#pragma unroll
-                for (int ci = 0; ci < 4; ++ci) {
-                    const int c = part * 32 + ci * 64;
-                    if (c >= d.nrows) break;
-                    const RowQuant mine = row_quant(__ldcg(p.amax + d.row0 + min(c + lane, d.nrows - 1)));
-                    if (d.mt == 0 && rank == 0 && quad == 0 && c + lane < d.nrows)
-                        p.out_scale[d.row0 + c + lane] = mine.scale;
-#pragma unroll
-                    for (int mm = 0; mm < 4; ++mm) {
-                        uint32_t q[2];   // tokens e = 0, 1: two outputs each, in the low half
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const int src = 8 * mm + 2 * ft + e;
-                            RowQuant rq;
-                            rq.pre = __shfl_sync(0xffffffffu, mine.pre, src);
-                            rq.amax = __shfl_sync(0xffffffffu, mine.amax, src);
-                            rq.inv = __shfl_sync(0xffffffffu, mine.inv, src);
-                            uint32_t n[2];
-                            quantize_n<false, 2>(&a[ci][2 * (2 * mm + e)], rq, n);
-                            q[e] = __byte_perm(n[0], n[1], 0x0040u);
-                        }
-                        const bool odd = fj & 1;
-                        const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? q[0] : q[1], 4);
-                        const uint32_t word = odd ? __byte_perm(got, q[1], 0x5410u) : __byte_perm(q[0], got, 0x5410u);
-                        const int tok = c + 8 * mm + 2 * ft + (odd ? 1 : 0);
-                        if (wvalid && tok < d.nrows)
-                            *reinterpret_cast<uint32_t*>(static_cast<int8_t*>(p.out) +
-                                                         static_cast<size_t>(d.row0 + tok) * (p.N / 2) +
-                                                         (w0 >> 1) + 2 * (fj & ~1)) = word;
-                    }
-                }
-                continue;
-            }
 #pragma unroll 1
-            for (int c = part * 32; c < d.nrows; c += 64) {
+            for (int c = part * 32; c < d.nrows; c += 32 * kParts) {
                 uint32_t lo[16], hi[16];
                 tmem_ld_16x256b_x4(tb + c, lo);                  // rows 4 fj, 4 fj + 1
                 tmem_ld_16x256b_x4(tb + (16u << 16) + c, hi);    // rows 4 fj + 2, 4 fj + 3
@@ -687,12 +564,11 @@ q8_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
 
 // ------------------------------------------------------------------------ host side
 
-// Launch in clusters of `cs` CTAs, programmatic stream serialisation allowed; cooperative:
-// every CTA resident at once, or the launch fails.
+// Launch in clusters of `cs` CTAs, programmatic stream serialisation allowed.
 template <typename... KArgs, typename... Args>
-cudaError_t launch_clusters(void (*kern)(KArgs...), int ctas, int cs, int threads, int smem, bool cooperative,
-                            cudaStream_t s, Args&&... args) {
-    cudaLaunchAttribute attr[3];
+cudaError_t launch_clusters(void (*kern)(KArgs...), int ctas, int cs, int threads, int smem, cudaStream_t s,
+                            Args&&... args) {
+    cudaLaunchAttribute attr[2];
     int n = 1;
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -701,11 +577,6 @@ cudaError_t launch_clusters(void (*kern)(KArgs...), int ctas, int cs, int thread
         attr[n].val.clusterDim.x = static_cast<unsigned>(cs);
         attr[n].val.clusterDim.y = 1;
         attr[n].val.clusterDim.z = 1;
-        ++n;
-    }
-    if (cooperative) {
-        attr[n].id = cudaLaunchAttributeCooperative;
-        attr[n].val.cooperative = 1;
         ++n;
     }
     cudaLaunchConfig_t cfg = {};
@@ -736,7 +607,7 @@ cudaError_t launch_stream(const CUtensorMap& w, const CUtensorMap& x, const Q8Pa
     static bool done[64] = {false};
     const cudaError_t e = set_smem(q8_stream_kernel<MODE, SPLIT>, stream_smem(SPLIT), done);
     if (e != cudaSuccess) return e;
-    return launch_clusters(q8_stream_kernel<MODE, SPLIT>, clusters * cs, cs, kSThreads, stream_smem(SPLIT), false, s, w, x, p, cs);
+    return launch_clusters(q8_stream_kernel<MODE, SPLIT>, clusters * cs, cs, kSThreads, stream_smem(SPLIT), s, w, x, p, cs);
 }
 
 // Pairs of CTAs that fit on the device at once, once per device (outside any capture: the
@@ -774,24 +645,8 @@ cudaError_t launch_pair(const CUtensorMap& w, const CUtensorMap& x, const Q8Para
     int most = 0;
     const cudaError_t e = max_pairs<MODE>(&most);
     if (e != cudaSuccess) return e;
-    // OUT_ACT8: the units of a token tile wait for one another, so every pair is resident
-    // (cooperative launch) and has at most one unit of a tile
-    const int MT = (p.N + 2 * kPWRows - 1) / (2 * kPWRows);
-    if (MODE == OUT_ACT8) {
-        if (most < MT) return cudaErrorInvalidConfiguration;
-        most -= most % MT;
-    }
-    const int pairs = units < most ? static_cast<int>(units) : most;   // OUT_ACT8: units is a multiple of MT
-    return launch_clusters(q8_pair_kernel<MODE>, 2 * pairs, 2, kPThreads, kPSmemBytes, MODE == OUT_ACT8, s, w, x, p);
-}
-
-// OUT_ACT8 runs where at most an eighth of the 74 pairs stay idle in groups of MT = ceil(2 I /
-// 256) (and never more than 74); else the activations go through float32 and the row
-// quantiser.
-constexpr int kPairsB200 = 74;
-bool act8_groups(int I) {
-    const int MT = (2 * I + 2 * kPWRows - 1) / (2 * kPWRows);
-    return MT <= kPairsB200 && 8 * (kPairsB200 % MT) <= kPairsB200;
+    const int pairs = units < most ? static_cast<int>(units) : most;
+    return launch_clusters(q8_pair_kernel<MODE>, 2 * pairs, 2, kPThreads, kPSmemBytes, s, w, x, p);
 }
 
 // Rows per expert up to which the streaming kernel runs (a chunk of it).
@@ -818,29 +673,21 @@ template <int MODE>
 cudaError_t product(const Q8GemmArgs& a, const Q8Params& p, cudaStream_t s) {
     CUtensorMap w, x;
     const bool chunked = a.swiglu && a.fc1_chunked;
-    if (MODE == OUT_ACT8 || static_cast<long long>(a.rows) > static_cast<long long>(kStreamRows) * a.E) {
+    if (static_cast<long long>(a.rows) > static_cast<long long>(kStreamRows) * a.E) {
         if (!tmap::quads8(&w, a.w_q, a.E, a.N, a.K, chunked)) return cudaErrorInvalidValue;
         if (!tmap::matrix8(&x, a.a_q, a.rows, a.K, kPBox)) return cudaErrorInvalidValue;
         const long long units = (static_cast<long long>((a.rows + kPTok - 1) / kPTok) + a.E) *
                                 ((a.N + 2 * kPWRows - 1) / (2 * kPWRows));
         return launch_pair<MODE>(w, x, p, units, s);
     }
-    if constexpr (MODE == OUT_ACT8) return cudaErrorInvalidValue;   // not reached
-    else return stream_product<MODE>(a, p, chunked, s);
+    return stream_product<MODE>(a, p, chunked, s);
 }
 }  // namespace
-
-bool q8_act8_supported(int rows, int E, int I) {
-    return static_cast<long long>(rows) > static_cast<long long>(kStreamRows) * E && act8_groups(I);
-}
-
-int q8_act8_tiles(int rows, int E) { return rows / kPTok + E + 1; }
 
 cudaError_t launch_q8_gemm(const Q8GemmArgs& a, cudaStream_t s) {
     if (a.rows <= 0) return cudaSuccess;
     const Q8Params p{a.offsets, a.E, a.rows, a.K, a.N, a.a_scale, a.w_scale, a.bias, a.out, a.err, a.act,
-                     a.fc1_chunked, a.act8_scale, a.act8_amax, a.act8_arrived};
-    if (a.swiglu && a.act8_scale) return product<OUT_ACT8>(a, p, s);
+                     a.fc1_chunked};
     if (a.swiglu) return product<OUT_SWIGLU>(a, p, s);
     return a.out_bf16 ? product<OUT_BF16>(a, p, s) : product<OUT_F32>(a, p, s);
 }

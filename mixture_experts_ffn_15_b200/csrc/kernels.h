@@ -206,14 +206,7 @@ struct Q8GemmArgs {
     bool fc1_chunked = false;          // swiglu: weight rows, scales and bias in the chunked layout
     void* out = nullptr;
     int32_t* err = nullptr;            // device error word or nullptr
-    // swiglu, with act8_scale (where q8_act8_supported): out [rows, N / 2] int8, the
-    // activations' rows cut to 8 bits in the same launch
-    float* act8_scale = nullptr;       // [rows] out
-    uint32_t* act8_amax = nullptr;     // [rows] scratch, zero on entry
-    int32_t* act8_arrived = nullptr;   // [q8_act8_tiles] scratch, zero on entry
 };
-bool q8_act8_supported(int rows, int E, int I);
-int q8_act8_tiles(int rows, int E);
 cudaError_t launch_q8_gemm(const Q8GemmArgs& a, cudaStream_t s);
 
 // ---------------------------------------------------------------- balance.cu

@@ -5,13 +5,13 @@
 // NaN and q = 0, so that whatever is multiplied with it comes out NaN, as it would in
 // floating point.
 //
-// The whole number is the exact one, for every float32 and bf16 input: v = x (127 / amax)
-// in float32 is within 127 * 2^-23 = 1.6e-5 of the exact quotient, so its rounding can be
-// wrong only where v lies within that distance of a half.  Values within 1e-4 of a half
-// (one in 5000) are decided by the sign of 254 |x| - (2 m + 1) amax, m the whole part: both
-// products are exact (float64 for float32 inputs, float32 for bf16 ones).  A first version
-// took the quotient of such values in float64, eight at a time: 309 us instead of the time
-// below, since most blocks had a warp that waited for the division.
+// The whole number is the exact one, for every float32 and bf16 input.  v = x (127 / amax) in
+// float32 is within 1.6e-5 of the exact quotient, so its rounding can be wrong only where v
+// lies within that distance of a half.  A thread that meets such a float32 value (one value
+// in 25000 is within 2e-5 of a half) does its part of the row again, deciding each such value
+// by the sign of 254 |x| - (2 m + 1) amax, m the whole part, exact in pairs of floats.  For
+// bf16 the first rounding is exact (quantize.cuh says why), which matters: x = amax / 2 is a
+// half, and one value in 600 of a normal row is.
 //
 // One pass over the row: a row's threads keep their vectors of 8 elements in registers
 // between the maximum and the rounding (rows longer than kRegVec vectors a thread read the
@@ -24,7 +24,6 @@ namespace moe {
 namespace {
 
 constexpr int kQThreads = 256;
-constexpr int kRegVec = 4;
 
 template <bool BF16>
 struct Vec8 {
@@ -64,8 +63,8 @@ struct Vec8 {
     }
 };
 
-// TPR threads (a power of two, 32 .. 256) share a row.
-template <bool BF16, int TPR>
+// TPR threads (a power of two, 32 .. 256) share a row, kRegVec vectors a thread in registers.
+template <bool BF16, int TPR, int kRegVec>
 __global__ void __launch_bounds__(kQThreads)
 quantize_rows_kernel(const void* __restrict__ x, int rows, int K, int8_t* __restrict__ q,
                      float* __restrict__ scale) {
@@ -104,34 +103,63 @@ quantize_rows_kernel(const void* __restrict__ x, int rows, int K, int8_t* __rest
     const RowQuant rq = row_quant(m);
     if (t == 0) scale[row] = rq.scale;
     uint2* out = reinterpret_cast<uint2*>(q) + row * nvec;
-    float f[8];
+    bool sure = ordinary(rq) && !(BF16 && bf16_exception(m));
+    if (sure) {
+        float far = 0.f, f[8];
+        auto put = [&](const Vec8<BF16>& w, int v) {
+            uint32_t n[8];
+            w.get(f);
 #pragma unroll
-    for (int j = 0; j < kRegVec; ++j)
-        if (t + j * TPR < nvec) {
-            r[j].get(f);
-            out[t + j * TPR] = quantize8<BF16>(f, rq);
+            for (int i = 0; i < 8; ++i) n[i] = quantize_fast<true>(f[i], 1.f, rq.inv, &far);
+            if (BF16) far = 0.f;
+            out[v] = make_uint2(pack_s8x4(n), pack_s8x4(n + 4));
+        };
+#pragma unroll
+        for (int j = 0; j < kRegVec; ++j)
+            if (t + j * TPR < nvec) put(r[j], t + j * TPR);
+        for (int v = t + kRegVec * TPR; v < nvec; v += TPR) {
+            Vec8<BF16> w;
+            w.load(x, row, nvec, v);
+            put(w, v);
         }
-    for (int v = t + kRegVec * TPR; v < nvec; v += TPR) {
-        Vec8<BF16> w;
-        w.load(x, row, nvec, v);
-        w.get(f);
-        out[v] = quantize8<BF16>(f, rq);
+        sure = far <= kSureDistance;
+    }
+    if (!sure) {
+#pragma unroll 1
+        for (int v = t; v < nvec; v += TPR) {
+            Vec8<BF16> w;
+            float f[8];
+            uint32_t n[8];
+            w.load(x, row, nvec, v);
+            w.get(f);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) n[i] = quantize_exact(f[i], rq.pre, rq.inv, rq.amax);
+            out[v] = make_uint2(pack_s8x4(n), pack_s8x4(n + 4));
+        }
     }
 }
 
 template <bool BF16>
 cudaError_t launch(const void* x, int rows, int K, int8_t* q, float* scale, cudaStream_t s) {
     const int nvec = K / 8;
-    // threads a row: what holds it in registers
+    auto go = [&](auto kern, int tpr) {
+        const int per = kQThreads / tpr;
+        return launch_k(kern, dim3(static_cast<unsigned>((rows + per - 1) / per)), dim3(kQThreads), 0, s, x, rows, K, q,
+                        scale);
+    };
+    // Many rows: as few threads a row as hold it in registers, for many loads in flight and
+    // no barrier.  Few rows (less than four blocks an SM): spread a row, for latency.
+    constexpr int kReg = BF16 ? 12 : 6, kFew = 4;
+    const long long sms = device_sm_count();
     int tpr = 32;
-    while (tpr < kQThreads && tpr * kRegVec < nvec) tpr *= 2;
-    const int per = kQThreads / tpr;
-    const dim3 grid(static_cast<unsigned>((rows + per - 1) / per)), block(kQThreads);
+    while (tpr < kQThreads && (tpr * kReg < nvec || (tpr < nvec && static_cast<long long>(rows) * tpr < 4 * kQThreads * sms)))
+        tpr *= 2;
+    const bool few = tpr * kFew >= nvec;
     switch (tpr) {
-        case 32: return launch_k(quantize_rows_kernel<BF16, 32>, grid, block, 0, s, x, rows, K, q, scale);
-        case 64: return launch_k(quantize_rows_kernel<BF16, 64>, grid, block, 0, s, x, rows, K, q, scale);
-        case 128: return launch_k(quantize_rows_kernel<BF16, 128>, grid, block, 0, s, x, rows, K, q, scale);
-        default: return launch_k(quantize_rows_kernel<BF16, 256>, grid, block, 0, s, x, rows, K, q, scale);
+        case 32: return few ? go(quantize_rows_kernel<BF16, 32, kFew>, 32) : go(quantize_rows_kernel<BF16, 32, kReg>, 32);
+        case 64: return few ? go(quantize_rows_kernel<BF16, 64, kFew>, 64) : go(quantize_rows_kernel<BF16, 64, kReg>, 64);
+        case 128: return few ? go(quantize_rows_kernel<BF16, 128, kFew>, 128) : go(quantize_rows_kernel<BF16, 128, kReg>, 128);
+        default: return few ? go(quantize_rows_kernel<BF16, 256, kFew>, 256) : go(quantize_rows_kernel<BF16, 256, kReg>, 256);
     }
 }
 
