@@ -312,9 +312,16 @@ q8_stream_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
 // columns).  The weight rows are loaded in fragment order (lane 8 q + j of a 32-lane
 // quadrant holds the quadrant's row 4 j + q), so that a 16x256b accumulator fragment gives a
 // thread four consecutive weight rows of two tokens, stored straight from registers.
-// A CTA's warps: 0 the TMA producer, 1 the MMA issuer (even CTA), then the epilogue.
-constexpr int kPEpi = 8;
-constexpr int kPThreads = 64 + 32 * kPEpi;
+// A CTA's warps: 0 the TMA producer, 1 the MMA issuer (even CTA), 2-17 the epilogue, 18 works
+// out the units a few ahead, 19 brings the next unit's scales and biases into shared memory.
+// While the MMAs run, their operand reads leave the shared memory's other users waiting (a
+// load or a shuffle takes ~330 cycles): the search for a unit's expert by the MMA thread
+// itself cost 3000 cycles a unit (of 14800 at K = 2816, of 5900 at K = 704), the scales
+// loaded by the epilogue 4200.  16 warps of epilogue instead of 8 halve its time a unit (4900
+// -> 2200 cycles at N = 256): it waits for tensor memory and for stores, not for issue slots.
+constexpr int kPEpi = 16;
+constexpr int kPThreads = 128 + 32 * kPEpi;
+constexpr int kPPlan = 8;                // units worked out ahead
 constexpr int kPWRows = 128;
 constexpr int kPTok = 256;
 constexpr int kPSlots = 6;
@@ -324,24 +331,22 @@ constexpr int kPABytes = kPWRows * kBK;
 constexpr int kPBox = kPTok / 2;
 constexpr int kPBBytes = kPBox * kBK;
 constexpr int kPAccCols = 256;
-constexpr int kPMiscBytes = (2 * kPStages + 4) * 8 + 16 + 2 * (kMaxExperts + 1) * 4 + 64;
+struct PScales {
+    float sa[kPTok];         // of the unit's tokens
+    float sw[kPWRows];       // of the CTA's weight rows
+    float bias[kPWRows];
+};
+constexpr int kPMiscBytes = 2 * static_cast<int>(sizeof(PScales)) + kPPlan * 32 + (2 * kPStages + 8) * 8 + 16 +
+                            2 * (kMaxExperts + 1) * 4 + 64;
 constexpr int kPSmemBytes = 1024 + kPSlots * (kPABytes + kPBBytes) + kPMiscBytes;
 static_assert(kPSmemBytes <= 227 * 1024, "shared memory");
 
-struct PUnit {
-    int g, row0, nrows, n, mt;   // expert, first row, rows, MMA N, weight tile
+// A unit as the planning warp hands it on: expert, first row, rows, weight tile.  The MMA's N
+// is rows rounded up to 32 (each CTA's half: a multiple of 16 rows).
+struct __align__(16) PUnit {
+    int g, row0, nrows, mt;
 };
-
-__device__ __forceinline__ PUnit pair_unit(long long u, int MT, int G, const int* s_off, const int* s_pre) {
-    PUnit d;
-    const int tile = static_cast<int>(u / MT);
-    d.mt = static_cast<int>(u - static_cast<long long>(tile) * MT);
-    d.g = tile_group(tile, G, s_pre);
-    d.row0 = s_off[d.g] + (tile - s_pre[d.g]) * kPTok;
-    d.nrows = min(kPTok, s_off[d.g + 1] - d.row0);
-    d.n = ((d.nrows + 31) / 32) * 32;   // each CTA's half: a multiple of 16 rows
-    return d;
-}
+__device__ __forceinline__ int unit_n(int nrows) { return (nrows + 31) / 32 * 32; }
 
 template <int MODE>
 __global__ void __launch_bounds__(kPThreads, 1)
@@ -352,11 +357,17 @@ q8_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
                                                ~static_cast<uintptr_t>(1023));
     uint8_t* sA = smem;
     uint8_t* sB = smem + kPSlots * kPABytes;
-    uint64_t* full = reinterpret_cast<uint64_t*>(sB + kPSlots * kPBBytes);
+    PScales* s_scales = reinterpret_cast<PScales*>(sB + kPSlots * kPBBytes);   // [2]
+    PUnit* s_unit = reinterpret_cast<PUnit*>(s_scales + 2);   // [kPPlan]
+    uint64_t* ufull = reinterpret_cast<uint64_t*>(s_unit + kPPlan);
+    uint64_t* uempty = ufull + kPPlan;
+    uint64_t* full = uempty + kPPlan;
     uint64_t* empty = full + kPStages;
     uint64_t* tfull = empty + kPStages;
     uint64_t* tempty = tfull + 2;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tempty + 2);
+    uint64_t* sfull = tempty + 2;
+    uint64_t* sempty = sfull + 2;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sempty + 2);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     int* s_off = reinterpret_cast<int*>(tmem_slot + 4);
     int* s_pre = s_off + (kMaxExperts + 1);
@@ -373,6 +384,12 @@ q8_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
         for (int a = 0; a < 2; ++a) {
             mbar_init(smem_u32(&tfull[a]), 1);
             mbar_init(smem_u32(&tempty[a]), 2 * kPEpi);   // both CTAs'
+            mbar_init(smem_u32(&sfull[a]), 1);
+            mbar_init(smem_u32(&sempty[a]), kPEpi);
+        }
+        for (int q = 0; q < kPPlan; ++q) {
+            mbar_init(smem_u32(&ufull[q]), 1);
+            mbar_init(smem_u32(&uempty[q]), kPEpi + (lead ? 3 : 2));   // producer, scales, epilogue, MMA
         }
         *abort_flag = 0;
         fence_mbar_init();
@@ -400,52 +417,70 @@ q8_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
     const int pair = static_cast<int>(blockIdx.x >> 1), npairs = static_cast<int>(gridDim.x >> 1);
     const int nk = (p.K + kBK - 1) / kBK;
 
+    // the planned units, as every role reads them: wait, read; free the slot once done
+    struct Plan {
+        int slot = 0;
+        uint32_t phase = 0;
+        __device__ __forceinline__ void next() {
+            if (++slot == kPPlan) {
+                slot = 0;
+                phase ^= 1u;
+            }
+        }
+    } plan;
+
     if (warp == 0) {
         // ------------------------------------------------------------ TMA producer
-        int stage = 0;
-        uint32_t phase = 0;
-        for (long long u = pair; u < units && !*abort_flag; u += npairs) {
-            const PUnit d = pair_unit(u, MT, G, s_off, s_pre);
-            const int trow0 = d.row0 + static_cast<int>(rank) * (d.n / 2);
-            // weight views: plain (k, j, q, Q, e) at (k, 0, 0, w_in / 32, g); chunked fc1
-            // (k, j, s, qq, X) at (k, 0, 0, 0, g I / 8 + w_in / 32)
-            const int w_in = d.mt * 2 * kPWRows + static_cast<int>(rank) * kPWRows;
-            const bool chunked = MODE == OUT_SWIGLU && p.chunked;
-            const int wc3 = chunked ? 0 : w_in / 32;
-            const int wc4 = chunked ? d.g * (p.N / 16) + w_in / 32 : d.g;
-            const uint32_t bytes = static_cast<uint32_t>(2 * (kPABytes + kPBBytes));
-            bool ok = true;
-            for (int kb0 = 0; kb0 < nk; kb0 += kPSub) {
-                const int ns = min(kPSub, nk - kb0);
-                if (lane == 0) {
+        if (lane == 0) {
+            int stage = 0;
+            uint32_t phase = 0;
+            for (long long u = pair; u < units && !*abort_flag; u += npairs, plan.next()) {
+                if (!mbar_wait(smem_u32(&ufull[plan.slot]), plan.phase, abort_flag, kWaitNs)) break;
+                const PUnit d = s_unit[plan.slot];
+                mbar_arrive(smem_u32(&uempty[plan.slot]));
+                const int trow0 = d.row0 + static_cast<int>(rank) * (unit_n(d.nrows) / 2);
+                // weight views: plain (k, j, q, Q, e) at (k, 0, 0, w_in / 32, g); chunked fc1
+                // (k, j, s, qq, X) at (k, 0, 0, 0, g I / 8 + w_in / 32)
+                const int w_in = d.mt * 2 * kPWRows + static_cast<int>(rank) * kPWRows;
+                const bool chunked = MODE == OUT_SWIGLU && p.chunked;
+                const int wc3 = chunked ? 0 : w_in / 32;
+                const int wc4 = chunked ? d.g * (p.N / 16) + w_in / 32 : d.g;
+                const uint32_t bytes = static_cast<uint32_t>(2 * (kPABytes + kPBBytes));
+                bool ok = true;
+                for (int kb0 = 0; kb0 < nk; kb0 += kPSub) {
+                    const int ns = min(kPSub, nk - kb0);
                     ok = mbar_wait(smem_u32(&empty[stage]), phase ^ 1u, abort_flag, kWaitNs);
-                    if (ok && lead) mbar_arrive_expect_tx(smem_u32(&full[stage]), static_cast<uint32_t>(ns) * bytes);
-                }
-                ok = __shfl_sync(0xffffffffu, ok, 0);
-                if (!ok) break;
-                const uint32_t fb = mapa_shared(smem_u32(&full[stage]), 0);   // the even CTA's
-                if (lane == 0) {
+                    if (!ok) break;
+                    if (lead) mbar_arrive_expect_tx(smem_u32(&full[stage]), static_cast<uint32_t>(ns) * bytes);
+                    const uint32_t fb = mapa_shared(smem_u32(&full[stage]), 0);   // the even CTA's
                     for (int j = 0; j < ns; ++j) {
                         const int sl = stage * kPSub + j, k0 = (kb0 + j) * kBK;
                         tma_load_5d_pair(smem_u32(sA + sl * kPABytes), &tmW, fb, k0, 0, 0, wc3, wc4);
                         tma_load_2d_pair(smem_u32(sB + sl * kPBBytes), &tmX, fb, k0, trow0);
                     }
+                    if (++stage == kPStages) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
                 }
-                if (++stage == kPStages) {
-                    stage = 0;
-                    phase ^= 1u;
-                }
+                if (!ok) break;
             }
-            if (!ok) break;
         }
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA issuer
         if (lead && lane == 0) {
             int stage = 0, acc = 0;
             uint32_t phase = 0, acc_phase = 0;
+            auto rows_of_next = [&]() {   // the next unit's rows, 0 if the wait gave up
+                int n = 0;
+                if (mbar_wait(smem_u32(&ufull[plan.slot]), plan.phase, abort_flag, kWaitNs)) n = s_unit[plan.slot].nrows;
+                mbar_arrive(smem_u32(&uempty[plan.slot]));
+                plan.next();
+                return n;
+            };
+            int nrows = pair < units ? rows_of_next() : 0, nrows_next = 0;
             for (long long u = pair; u < units && !*abort_flag; u += npairs) {
-                const PUnit d = pair_unit(u, MT, G, s_off, s_pre);
-                const uint32_t idesc = idesc_s8_s32(2 * kPWRows, d.n);
+                const uint32_t idesc = idesc_s8_s32(2 * kPWRows, unit_n(nrows));
                 if (!mbar_wait(smem_u32(&tempty[acc]), acc_phase ^ 1u, abort_flag, kWaitNs)) break;
                 tc_fence_after();
                 const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * kPAccCols);
@@ -462,20 +497,71 @@ q8_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
                         const uint32_t a0 = smem_u32(sA + sl * kPABytes), b0 = smem_u32(sB + sl * kPBBytes);
 #pragma unroll
                         for (int kk = 0; kk < kBK / 32; ++kk)
-                            umma_s8_pair(d_tmem, smem_desc_sw128(a0 + kk * 32), smem_desc_sw128(b0 + kk * 32), idesc,
-                                         (kb0 + j > 0 || kk > 0) ? 1u : 0u);
+                            if ((kb0 + j) * kBK + kk * 32 < p.K)   // nothing but zeros past K
+                                umma_s8_pair(d_tmem, smem_desc_sw128(a0 + kk * 32), smem_desc_sw128(b0 + kk * 32), idesc,
+                                             (kb0 + j > 0 || kk > 0) ? 1u : 0u);
                     }
                     umma_commit_pair(smem_u32(&empty[stage]), 0x3);
                     if (++stage == kPStages) {
                         stage = 0;
                         phase ^= 1u;
                     }
+                    // read behind the first MMAs, used after the last
+                    if (kb0 == 0 && u + npairs < units) nrows_next = rows_of_next();
                 }
                 if (!ok) break;
                 umma_commit_pair(smem_u32(&tfull[acc]), 0x3);
                 acc ^= 1;
                 if (acc == 0) acc_phase ^= 1u;
+                nrows = nrows_next;
             }
+        }
+    } else if (warp == 2 + kPEpi) {
+        // ------------------------------------------------------------ the units, ahead
+        if (lane == 0) {
+            for (long long u = pair; u < units && !*abort_flag; u += npairs, plan.next()) {
+                const int tile = static_cast<int>(u / MT);
+                PUnit d;
+                d.mt = static_cast<int>(u - static_cast<long long>(tile) * MT);
+                d.g = tile_group(tile, G, s_pre);
+                d.row0 = s_off[d.g] + (tile - s_pre[d.g]) * kPTok;
+                d.nrows = min(kPTok, s_off[d.g + 1] - d.row0);
+                if (!mbar_wait(smem_u32(&uempty[plan.slot]), plan.phase ^ 1u, abort_flag, kWaitNs)) break;
+                s_unit[plan.slot] = d;
+                mbar_arrive(smem_u32(&ufull[plan.slot]));
+            }
+        }
+    } else if (warp == 3 + kPEpi) {
+        // ------------------------------------------------------------ scales, a unit ahead
+        int acc = 0;
+        uint32_t acc_phase = 0;
+        for (long long u = pair; u < units && !*abort_flag; u += npairs, plan.next()) {
+            if (!mbar_wait(smem_u32(&ufull[plan.slot]), plan.phase, abort_flag, kWaitNs)) break;
+            const PUnit d = s_unit[plan.slot];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&uempty[plan.slot]));
+            const int w0 = d.mt * 2 * kPWRows + static_cast<int>(rank) * kPWRows;
+            float a8[kPTok / 32], w8[kPWRows / 32], b8[kPWRows / 32];
+#pragma unroll
+            for (int i = 0; i < kPTok / 32; ++i) a8[i] = __ldg(p.sa + d.row0 + min(lane + 32 * i, d.nrows - 1));
+#pragma unroll
+            for (int i = 0; i < kPWRows / 32; ++i) {
+                w8[i] = b8[i] = 0.f;
+                if (w0 + 32 * i < p.N) channel<MODE>(p, d.g, w0 + lane + 32 * i, &w8[i], &b8[i]);
+            }
+            if (!mbar_wait(smem_u32(&sempty[acc]), acc_phase ^ 1u, abort_flag, kWaitNs)) break;
+            PScales& sc = s_scales[acc];
+#pragma unroll
+            for (int i = 0; i < kPTok / 32; ++i) sc.sa[lane + 32 * i] = a8[i];
+#pragma unroll
+            for (int i = 0; i < kPWRows / 32; ++i) {
+                sc.sw[lane + 32 * i] = w8[i];
+                sc.bias[lane + 32 * i] = b8[i];
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&sfull[acc]));
+            acc ^= 1;
+            if (acc == 0) acc_phase ^= 1u;
         }
     } else {
         // ------------------------------------------------------------ epilogue
@@ -488,30 +574,34 @@ q8_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
         int acc = 0;
         uint32_t acc_phase = 0;
         for (long long u = pair; u < units && !*abort_flag; u += npairs) {
-            const PUnit d = pair_unit(u, MT, G, s_off, s_pre);
+            if (!mbar_wait(smem_u32(&ufull[plan.slot]), plan.phase, abort_flag, kWaitNs)) break;
+            const PUnit d = s_unit[plan.slot];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&uempty[plan.slot]));
+            plan.next();
             const int w0 = d.mt * 2 * kPWRows + static_cast<int>(rank) * kPWRows + quad * 32;
             const bool wvalid = w0 < p.N;   // N is a multiple of 32: the warp's rows are all valid or none
             const int wr = w0 + 4 * fj;
-            float sw[4] = {0.f, 0.f, 0.f, 0.f}, bias[4] = {0.f, 0.f, 0.f, 0.f};
-            if (wvalid) {
-#pragma unroll
-                for (int q = 0; q < 4; ++q) channel<MODE>(p, d.g, wr + q, &sw[q], &bias[q]);
-            }
+            if (!mbar_wait(smem_u32(&sfull[acc]), acc_phase, abort_flag, kWaitNs)) break;
+            const PScales& sc = s_scales[acc];
+            const float4 sw4 = *reinterpret_cast<const float4*>(sc.sw + quad * 32 + 4 * fj);
+            const float4 b4 = *reinterpret_cast<const float4*>(sc.bias + quad * 32 + 4 * fj);
+            const float sw[4] = {sw4.x, sw4.y, sw4.z, sw4.w}, bias[4] = {b4.x, b4.y, b4.z, b4.w};
+            constexpr int kChunks = kPTok / (32 * kParts);
             if (!mbar_wait(smem_u32(&tfull[acc]), acc_phase, abort_flag, kWaitNs)) break;
             tc_fence_after();
             const uint32_t tb = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) +
                                 static_cast<uint32_t>(acc * kPAccCols);
-#pragma unroll 1
-            for (int c = part * 32; c < d.nrows; c += 32 * kParts) {
+#pragma unroll
+            for (int ci = 0; ci < kChunks; ++ci) {
+                const int c = 32 * (part + ci * kParts);
+                if (c >= d.nrows) break;
                 uint32_t lo[16], hi[16];
                 tmem_ld_16x256b_x4(tb + c, lo);                  // rows 4 fj, 4 fj + 1
                 tmem_ld_16x256b_x4(tb + (16u << 16) + c, hi);    // rows 4 fj + 2, 4 fj + 3
-                float sa[8];
+                float2 sa2[4];
 #pragma unroll
-                for (int m = 0; m < 4; ++m)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e)
-                        sa[2 * m + e] = __ldg(p.sa + d.row0 + min(c + 8 * m + 2 * ft + e, d.nrows - 1));
+                for (int m = 0; m < 4; ++m) sa2[m] = *reinterpret_cast<const float2*>(sc.sa + c + 8 * m + 2 * ft);
                 tmem_wait_ld();
                 if (!wvalid) continue;
 #pragma unroll
@@ -519,7 +609,7 @@ q8_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         const int tok = c + 8 * m + 2 * ft + e;
-                        const float s = sa[2 * m + e];
+                        const float s = e ? sa2[m].y : sa2[m].x;
                         const float x0 = fmaf(static_cast<float>(static_cast<int>(lo[4 * m + e])), s * sw[0], bias[0]);
                         const float x1 = fmaf(static_cast<float>(static_cast<int>(lo[4 * m + 2 + e])), s * sw[1], bias[1]);
                         const float x2 = fmaf(static_cast<float>(static_cast<int>(hi[4 * m + e])), s * sw[2], bias[2]);
@@ -541,7 +631,10 @@ q8_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&tempty[acc]), 0));
+            if (lane == 0) {
+                mbar_arrive_cluster(mapa_shared(smem_u32(&tempty[acc]), 0));
+                mbar_arrive(smem_u32(&sempty[acc]));
+            }
             acc ^= 1;
             if (acc == 0) acc_phase ^= 1u;
         }
