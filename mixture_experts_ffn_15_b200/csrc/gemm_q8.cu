@@ -328,8 +328,8 @@ constexpr int kPSlots = 6;
 constexpr int kPSub = 2;
 constexpr int kPStages = kPSlots / kPSub;
 constexpr int kPABytes = kPWRows * kBK;
-constexpr int kPBox = kPTok / 2;
-constexpr int kPBBytes = kPBox * kBK;
+constexpr int kPBox = 32;                // token rows per TMA box
+constexpr int kPBBytes = kPTok / 2 * kBK;
 constexpr int kPAccCols = 256;
 struct PScales {
     float sa[kPTok];         // of the unit's tokens
@@ -445,7 +445,10 @@ q8_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
                 const bool chunked = MODE == OUT_SWIGLU && p.chunked;
                 const int wc3 = chunked ? 0 : w_in / 32;
                 const int wc4 = chunked ? d.g * (p.N / 16) + w_in / 32 : d.g;
-                const uint32_t bytes = static_cast<uint32_t>(2 * (kPABytes + kPBBytes));
+                // the CTA's half of the tokens in boxes of 32 rows: the MMA's time goes by the
+                // shared memory's (operand reads and these writes), so no rows past the tile
+                const int nb = (unit_n(d.nrows) / 2 + kPBox - 1) / kPBox;
+                const uint32_t bytes = static_cast<uint32_t>(2 * (kPABytes + nb * kPBox * kBK));
                 bool ok = true;
                 for (int kb0 = 0; kb0 < nk; kb0 += kPSub) {
                     const int ns = min(kPSub, nk - kb0);
@@ -456,7 +459,8 @@ q8_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
                     for (int j = 0; j < ns; ++j) {
                         const int sl = stage * kPSub + j, k0 = (kb0 + j) * kBK;
                         tma_load_5d_pair(smem_u32(sA + sl * kPABytes), &tmW, fb, k0, 0, 0, wc3, wc4);
-                        tma_load_2d_pair(smem_u32(sB + sl * kPBBytes), &tmX, fb, k0, trow0);
+                        for (int i = 0; i < nb; ++i)
+                            tma_load_2d_pair(smem_u32(sB + sl * kPBBytes) + i * kPBox * kBK, &tmX, fb, k0, trow0 + i * kPBox);
                     }
                     if (++stage == kPStages) {
                         stage = 0;
@@ -573,32 +577,43 @@ q8_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
         const int fj = lane >> 2, ft = lane & 3;
         int acc = 0;
         uint32_t acc_phase = 0;
-        for (long long u = pair; u < units && !*abort_flag; u += npairs) {
-            if (!mbar_wait(smem_u32(&ufull[plan.slot]), plan.phase, abort_flag, kWaitNs)) break;
-            const PUnit d = s_unit[plan.slot];
+        // the unit after the current one, read behind the current one's first loads
+        auto read_unit = [&](PUnit* d) {
+            if (!mbar_wait(smem_u32(&ufull[plan.slot]), plan.phase, abort_flag, kWaitNs)) return false;
+            *d = s_unit[plan.slot];
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&uempty[plan.slot]));
             plan.next();
+            return true;
+        };
+        PUnit d, d_next{0, 0, 0, 0};
+        bool ok = pair >= units || read_unit(&d);
+        for (long long u = pair; ok && u < units && !*abort_flag; u += npairs) {
             const int w0 = d.mt * 2 * kPWRows + static_cast<int>(rank) * kPWRows + quad * 32;
             const bool wvalid = w0 < p.N;   // N is a multiple of 32: the warp's rows are all valid or none
             const int wr = w0 + 4 * fj;
+            constexpr int kChunks = kPTok / (32 * kParts);
             if (!mbar_wait(smem_u32(&sfull[acc]), acc_phase, abort_flag, kWaitNs)) break;
             const PScales& sc = s_scales[acc];
-            const float4 sw4 = *reinterpret_cast<const float4*>(sc.sw + quad * 32 + 4 * fj);
-            const float4 b4 = *reinterpret_cast<const float4*>(sc.bias + quad * 32 + 4 * fj);
-            const float sw[4] = {sw4.x, sw4.y, sw4.z, sw4.w}, bias[4] = {b4.x, b4.y, b4.z, b4.w};
-            constexpr int kChunks = kPTok / (32 * kParts);
             if (!mbar_wait(smem_u32(&tfull[acc]), acc_phase, abort_flag, kWaitNs)) break;
             tc_fence_after();
             const uint32_t tb = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) +
                                 static_cast<uint32_t>(acc * kPAccCols);
+            float4 sw, bias;
 #pragma unroll
             for (int ci = 0; ci < kChunks; ++ci) {
                 const int c = 32 * (part + ci * kParts);
-                if (c >= d.nrows) break;
                 uint32_t lo[16], hi[16];
-                tmem_ld_16x256b_x4(tb + c, lo);                  // rows 4 fj, 4 fj + 1
-                tmem_ld_16x256b_x4(tb + (16u << 16) + c, hi);    // rows 4 fj + 2, 4 fj + 3
+                if (c < d.nrows) {
+                    tmem_ld_16x256b_x4(tb + c, lo);                  // rows 4 fj, 4 fj + 1
+                    tmem_ld_16x256b_x4(tb + (16u << 16) + c, hi);    // rows 4 fj + 2, 4 fj + 3
+                }
+                if (ci == 0) {
+                    sw = *reinterpret_cast<const float4*>(sc.sw + quad * 32 + 4 * fj);
+                    bias = *reinterpret_cast<const float4*>(sc.bias + quad * 32 + 4 * fj);
+                    if (u + npairs < units) ok = read_unit(&d_next);
+                }
+                if (c >= d.nrows) break;
                 float2 sa2[4];
 #pragma unroll
                 for (int m = 0; m < 4; ++m) sa2[m] = *reinterpret_cast<const float2*>(sc.sa + c + 8 * m + 2 * ft);
@@ -610,10 +625,10 @@ q8_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
                     for (int e = 0; e < 2; ++e) {
                         const int tok = c + 8 * m + 2 * ft + e;
                         const float s = e ? sa2[m].y : sa2[m].x;
-                        const float x0 = fmaf(static_cast<float>(static_cast<int>(lo[4 * m + e])), s * sw[0], bias[0]);
-                        const float x1 = fmaf(static_cast<float>(static_cast<int>(lo[4 * m + 2 + e])), s * sw[1], bias[1]);
-                        const float x2 = fmaf(static_cast<float>(static_cast<int>(hi[4 * m + e])), s * sw[2], bias[2]);
-                        const float x3 = fmaf(static_cast<float>(static_cast<int>(hi[4 * m + 2 + e])), s * sw[3], bias[3]);
+                        const float x0 = fmaf(static_cast<float>(static_cast<int>(lo[4 * m + e])), s * sw.x, bias.x);
+                        const float x1 = fmaf(static_cast<float>(static_cast<int>(lo[4 * m + 2 + e])), s * sw.y, bias.y);
+                        const float x2 = fmaf(static_cast<float>(static_cast<int>(hi[4 * m + e])), s * sw.z, bias.z);
+                        const float x3 = fmaf(static_cast<float>(static_cast<int>(hi[4 * m + 2 + e])), s * sw.w, bias.w);
                         if (tok < d.nrows) {
                             const size_t row = static_cast<size_t>(d.row0 + tok);
                             if constexpr (MODE == OUT_SWIGLU)
@@ -637,6 +652,7 @@ q8_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
             }
             acc ^= 1;
             if (acc == 0) acc_phase ^= 1u;
+            d = d_next;
         }
     }
 
