@@ -127,10 +127,11 @@ bool valid_w8a8_ffn(int H, int I) {
     return H > 0 && I > 0 && H % 32 == 0 && I % 32 == 0 && H <= kQ8MaxK && I <= kQ8MaxK;
 }
 
-// Workspace of the int8 expert FFN: error word, the int8 rows and scales of x_perm, the
-// float32 activations, their int8 rows and scales.
+// Workspace of the int8 expert FFN: error word and, for few rows per expert, the counters of
+// its one launch (both cleared by the row quantiser), the int8 rows and scales of x_perm,
+// the float32 activations, their int8 rows and scales.
 struct W8a8Layout {
-    size_t err, xq, xs, act, aq, as, total;
+    size_t err, counters, clear_end, xq, xs, act, aq, as, total;
 };
 
 W8a8Layout w8a8_layout(int rows, int H, int E, int I) {
@@ -138,6 +139,8 @@ W8a8Layout w8a8_layout(int rows, int H, int E, int I) {
     Carver c;
     W8a8Layout L;
     L.err = c.take(kAlign);
+    L.counters = c.take(q8_ffn_supported(rows, E) ? static_cast<size_t>(q8_ffn_counters(rows, E)) * 4 : 0);
+    L.clear_end = c.off;
     L.xq = c.take(r * H);
     L.xs = c.take(r * 4);
     L.act = c.take(r * I * 4);
@@ -787,8 +790,32 @@ static moe_status w8a8_ffn(const void* x_perm, const int32_t* offsets, const int
     float* act = reinterpret_cast<float*>(ws + L.act);
     int8_t* aq = reinterpret_cast<int8_t*>(ws + L.aq);
     float* as = reinterpret_cast<float*>(ws + L.as);
-    MOE_CUDA(launch_clear(ws + L.err, kAlign, s));
-    MOE_CUDA(launch_quantize_rows(x_perm, rows, H, true, xq, xs, s));
+    MOE_CUDA(launch_quantize_rows(x_perm, rows, H, true, xq, xs, s, reinterpret_cast<int32_t*>(ws + L.err),
+                                  static_cast<int>((L.clear_end - L.err) / 4)));
+    if (q8_ffn_supported(rows, E)) {
+        Q8FfnArgs f;
+        f.x_q = xq;
+        f.x_scale = xs;
+        f.offsets = offsets;
+        f.fc1_q = fc1_q;
+        f.fc2_q = fc2_q;
+        f.rows = rows;
+        f.H = H;
+        f.E = E;
+        f.I = I;
+        f.ep = ep;
+        f.ep.fc1_scale = fc1_scale;
+        f.ep.fc2_scale = fc2_scale;
+        f.act = act;
+        f.act_q = aq;
+        f.act_scale = as;
+        f.counters = reinterpret_cast<int32_t*>(ws + L.counters);
+        f.err = err;
+        f.y = y_perm;
+        MOE_CUDA(launch_q8_ffn(f, s));
+        if (mid) record_event(mid, s);
+        return MOE_OK;
+    }
     Q8GemmArgs g;
     g.a_q = xq;
     g.a_scale = xs;

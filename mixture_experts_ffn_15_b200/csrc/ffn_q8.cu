@@ -1,0 +1,499 @@
+// Expert FFN with int8 activations and weights for few rows per expert, in one launch:
+//   fc1 (int8 x int8) + SwiGLU -> rows cut to int8 -> fc2 (int8 x int8)
+// The arithmetic is that of gemm_q8.cu and quantize.cu; x_perm arrives as int8 rows.
+//
+// 128 weight rows on the MMA's M side, a chunk of up to 64 token rows of one expert on N, so
+// that every weight byte streams from HBM once; bound by that stream.  The unit list holds
+// every fc1 unit (chunk x 128 rows of fc1), then the rounding units (up to 8 rows of a chunk's
+// activations), then every fc2 unit.  A CTA's first unit is unit blockIdx.x, later ones come
+// in list order from a counter (starting at the grid size), so the long fc1 units go first
+// and the short fc2 units even out the end.  (The rounding by the one warp that completes a
+// chunk, without units of its own, took 576 us instead of @@ at 2048 rows: 64 rows are too
+// many for a warp.)
+//
+// Warps of a CTA:
+//   0    claims the units and streams their weights (TMA) into the ring.  Weights depend on
+//        nothing this launch or the quantiser in front of it writes: the first unit's loads
+//        start before that kernel has finished, and those of an fc2 unit before its
+//        activations exist.
+//   1    issues the MMAs (tcgen05 kind::i8) into one of two accumulators
+//   2-5  epilogue.  fc1: the activations in float32 to scratch.  Rounding: two rows a warp,
+//        once every fc1 unit of the chunk has been here (a counter).  fc2: scales, bias,
+//        bf16 outputs.
+//   6    streams the token rows: x's, or a chunk's activations once they are published
+// The launch is cooperative (every CTA resident), so a unit waited for is some running CTA's.
+// Every wait is bounded (2 s) and reports MOE_DEVERR_TIMEOUT.
+#include <cuda.h>
+
+#include "common.cuh"
+#include "kernels.h"
+#include "quantize.cuh"
+#include "sm100.cuh"
+#include "tile_map.cuh"
+#include "tmap.cuh"
+
+namespace moe {
+namespace {
+
+using namespace sm100;
+
+constexpr int kBK = tmap::kBoxK8;
+constexpr int kTok = 64;                 // token rows per chunk
+constexpr int kBox = 16;                 // token rows per TMA box
+constexpr int kWRows = 128;
+constexpr int kSub = 2;                  // ring slots per barrier stage
+constexpr int kStages = 4;
+constexpr int kSlots = kStages * kSub;
+constexpr int kABytes = kWRows * kBK;
+constexpr int kBBytes = kTok * kBK;
+constexpr int kRing = 8;                 // claimed units handed to the other warps
+constexpr int kThreads = 224;
+constexpr uint64_t kWaitNs = 2000000000ull;
+constexpr int kMiscBytes = kRing * 32 + (2 * kStages + 4 + 2 * kRing) * 8 + 16 + 2 * (kMaxExperts + 1) * 4 + 64;
+constexpr int kSmemBytes = 1024 + kSlots * (kABytes + kBBytes) + kMiscBytes;
+static_assert(kSmemBytes <= 227 * 1024, "shared memory");
+
+struct Params {
+    const int32_t* offsets;   // [E+1] device
+    int E, rows, H, I;
+    const float* xs;          // [rows] scales of the int8 rows of x
+    const float* s1;          // [E, 2I]
+    const float* s2;          // [E, H]
+    const __nv_bfloat16* b1;  // [E, 2I] or nullptr
+    const __nv_bfloat16* b2;  // [E, H] or nullptr
+    float* act;               // [rows, I] scratch
+    int8_t* aq;               // [rows, I] scratch
+    float* as;                // [rows] scratch
+    __nv_bfloat16* y;         // [rows, H]
+    int32_t* done;            // [chunks] finished fc1 epilogue warps, zero on entry
+    int32_t* ready;           // [chunks] rows whose int8 activations are there, zero on entry
+    int32_t* sched;           // units claimed past the first gridDim.x, zero on entry
+    int32_t* err;
+    SwigluAttr attr;
+    bool chunked;
+};
+
+struct __align__(16) Unit {
+    int g, row0, nrows, mt;   // expert, first row, rows, weight tile
+    int chunk, kind;
+    int pad[2];
+};
+enum Kind : int { kNone = -1, kFc2 = 0, kFc1 = 1, kRound = 2 };
+constexpr int kRoundRows = 8;            // rows of a rounding unit: two for each epilogue warp
+constexpr int kRounds = kTok / kRoundRows;
+
+__device__ __forceinline__ int ld_acquire(const int32_t* p) {
+    int v;
+    asm volatile("ld.acquire.gpu.global.b32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+    return v;
+}
+
+// Bounded wait for *ctr >= target, by one lane.
+__device__ __forceinline__ bool wait_count(const int32_t* ctr, int target, volatile int* abort) {
+    if (ld_acquire(ctr) >= target) return true;
+    const uint64_t t0 = global_timer_ns();
+    for (;;) {
+        __nanosleep(32);
+        if (ld_acquire(ctr) >= target) return true;
+        if (*abort) return false;
+        if (global_timer_ns() - t0 > kWaitNs) {
+            *abort = 1;
+            return false;
+        }
+    }
+}
+
+__device__ __forceinline__ void fence_proxy_async_global() { asm volatile("fence.proxy.async.global;" ::: "memory"); }
+
+// The int8 rows of activation rows row and row + 1 (if `two`), by one warp; a row is read
+// twice (its maximum, then its values), both times from L2.
+__device__ __forceinline__ void round_rows(const Params& p, int row, bool two, int lane) {
+    const int nvec = p.I / 4;
+    const float4* x0 = reinterpret_cast<const float4*>(p.act + static_cast<size_t>(row) * p.I);
+    const float4* x1 = two ? x0 + nvec : x0;
+    uint32_t m0 = 0, m1 = 0;
+    auto top = [](const float4& v) {
+        return max(max(__float_as_uint(v.x) & 0x7fffffffu, __float_as_uint(v.y) & 0x7fffffffu),
+                   max(__float_as_uint(v.z) & 0x7fffffffu, __float_as_uint(v.w) & 0x7fffffffu));
+    };
+#pragma unroll 4
+    for (int v = lane; v < nvec; v += 32) {
+        m0 = max(m0, top(__ldcg(x0 + v)));
+        m1 = max(m1, top(__ldcg(x1 + v)));
+    }
+    const RowQuant q0 = row_quant(__reduce_max_sync(0xffffffffu, m0));
+    const RowQuant q1 = row_quant(__reduce_max_sync(0xffffffffu, m1));
+    uint32_t* out = reinterpret_cast<uint32_t*>(p.aq + static_cast<size_t>(row) * p.I);
+    float far = ordinary(q0) && ordinary(q1) ? 0.f : 1.f;
+    auto fast = [&](const float4& v, const RowQuant& q) {
+        const uint32_t n[4] = {quantize_fast<true>(v.x, 1.f, q.inv, &far), quantize_fast<true>(v.y, 1.f, q.inv, &far),
+                               quantize_fast<true>(v.z, 1.f, q.inv, &far), quantize_fast<true>(v.w, 1.f, q.inv, &far)};
+        return pack_s8x4(n);
+    };
+#pragma unroll 4
+    for (int v = lane; v < nvec; v += 32) {
+        out[v] = fast(__ldcg(x0 + v), q0);
+        if (two) out[nvec + v] = fast(__ldcg(x1 + v), q1);
+    }
+    if (!(far <= kSureDistance)) {   // this lane's values again, exactly
+        auto exact = [](const float4& v, const RowQuant& q) {
+            const uint32_t n[4] = {quantize_exact(v.x, q.pre, q.inv, q.amax), quantize_exact(v.y, q.pre, q.inv, q.amax),
+                                   quantize_exact(v.z, q.pre, q.inv, q.amax), quantize_exact(v.w, q.pre, q.inv, q.amax)};
+            return pack_s8x4(n);
+        };
+#pragma unroll 1
+        for (int v = lane; v < nvec; v += 32) {
+            out[v] = exact(__ldcg(x0 + v), q0);
+            if (two) out[nvec + v] = exact(__ldcg(x1 + v), q1);
+        }
+    }
+    if (lane == 0) {
+        p.as[row] = q0.scale;
+        if (two) p.as[row + 1] = q1.scale;
+    }
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+q8_ffn_kernel(const __grid_constant__ CUtensorMap tmW1, const __grid_constant__ CUtensorMap tmX,
+              const __grid_constant__ CUtensorMap tmW2, const __grid_constant__ CUtensorMap tmA, const Params p) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                               ~static_cast<uintptr_t>(1023));
+    uint8_t* sA = smem;
+    uint8_t* sB = smem + kSlots * kABytes;
+    Unit* s_unit = reinterpret_cast<Unit*>(sB + kSlots * kBBytes);   // [kRing]
+    uint64_t* full = reinterpret_cast<uint64_t*>(s_unit + kRing);
+    uint64_t* empty = full + kStages;
+    uint64_t* tfull = empty + kStages;
+    uint64_t* tempty = tfull + 2;
+    uint64_t* ufull = tempty + 2;
+    uint64_t* uempty = ufull + kRing;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(uempty + kRing);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    int* s_off = reinterpret_cast<int*>(tmem_slot + 4);
+    int* s_pre = s_off + (kMaxExperts + 1);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(smem_u32(&full[s]), 2);    // the weights' and the tokens' producer
+            mbar_init(smem_u32(&empty[s]), 1);
+        }
+        for (int a = 0; a < 2; ++a) {
+            mbar_init(smem_u32(&tfull[a]), 1);
+            mbar_init(smem_u32(&tempty[a]), 4);
+        }
+        for (int q = 0; q < kRing; ++q) {
+            mbar_init(smem_u32(&ufull[q]), 1);
+            mbar_init(smem_u32(&uempty[q]), 6);  // MMA, tokens, 4 epilogue warps
+        }
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 0 && lane == 0) {
+        tma_prefetch_desc(&tmW1);
+        tma_prefetch_desc(&tmW2);
+        tma_prefetch_desc(&tmX);
+        tma_prefetch_desc(&tmA);
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_u32(tmem_slot), 2 * kTok);
+        tmem_relinquish();
+    }
+    // The kernel in front is the row quantiser of the same call, which lets this one start
+    // only after all work before it has completed: the offsets and the weights are final.
+    // What the quantiser writes (int8 rows, scales, cleared counters, the error word) is
+    // read, and anything is written, only after pdl_wait.
+    pdl_trigger();
+    if (warp == 2) build_group_tiles(p.offsets, p.rows, nullptr, p.E, kTok, s_off, s_pre, lane);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+
+    const int MT1 = (2 * p.I + kWRows - 1) / kWRows, MT2 = (p.H + kWRows - 1) / kWRows;
+    const int chunks = s_pre[p.E];
+    const int U1 = chunks * MT1, U2 = U1 + chunks * kRounds, U = U2 + chunks * MT2;
+    const int nk1 = (p.H + kBK - 1) / kBK, nk2 = (p.I + kBK - 1) / kBK;
+
+    int slot = 0;
+    uint32_t uphase = 0;
+    auto next_slot = [&]() {
+        if (++slot == kRing) {
+            slot = 0;
+            uphase ^= 1u;
+        }
+    };
+    // the next claimed unit, as every warp but the claiming one reads it (one lane or all)
+    auto next_unit = [&](Unit* d, bool whole_warp) {
+        if (!mbar_wait(smem_u32(&ufull[slot]), uphase, abort_flag, kWaitNs)) return false;
+        *d = s_unit[slot];
+        if (whole_warp) __syncwarp();
+        if (!whole_warp || lane == 0) mbar_arrive(smem_u32(&uempty[slot]));
+        next_slot();
+        return d->kind != kNone;
+    };
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ claims, weights
+        if (lane == 0) {
+            int stage = 0;
+            uint32_t phase = 0;
+            bool first = true;
+            for (;;) {
+                if (!mbar_wait(smem_u32(&uempty[slot]), uphase ^ 1u, abort_flag, kWaitNs)) break;
+                int u = static_cast<int>(blockIdx.x);
+                if (!first) u = static_cast<int>(gridDim.x) + atomicAdd(p.sched, 1);
+                Unit d;
+                d.kind = u >= U ? kNone : u < U1 ? kFc1 : u < U2 ? kRound : kFc2;
+                if (d.kind != kNone) {
+                    const int v = d.kind == kFc1 ? u : d.kind == kRound ? u - U1 : u - U2;
+                    const int MT = d.kind == kFc1 ? MT1 : d.kind == kRound ? kRounds : MT2;
+                    d.chunk = v / MT;
+                    d.mt = v - d.chunk * MT;
+                    d.g = tile_group(d.chunk, p.E, s_pre);
+                    d.row0 = s_off[d.g] + (d.chunk - s_pre[d.g]) * kTok;
+                    d.nrows = min(kTok, s_off[d.g + 1] - d.row0);
+                    if (d.kind == kRound && d.mt * kRoundRows >= d.nrows) {
+                        // no such rows: claim the next
+                        if (first) pdl_wait();
+                        first = false;
+                        continue;
+                    }
+                }
+                s_unit[slot] = d;
+                mbar_arrive(smem_u32(&ufull[slot]));
+                next_slot();
+                if (d.kind == kNone) break;
+                if (d.kind == kRound) {
+                    if (first) pdl_wait();
+                    first = false;
+                    continue;
+                }
+                // one load instruction for both weight tensors, its map chosen at run time
+                const CUtensorMap* mw = d.kind == kFc1 ? &tmW1 : &tmW2;
+                const int nk = d.kind == kFc1 ? nk1 : nk2;
+                bool ok = true;
+                for (int kb0 = 0; kb0 < nk; kb0 += kSub) {
+                    const int ns = min(kSub, nk - kb0);
+                    ok = mbar_wait(smem_u32(&empty[stage]), phase ^ 1u, abort_flag, kWaitNs);
+                    if (!ok) break;
+                    const uint32_t fb = smem_u32(&full[stage]);
+                    mbar_arrive_expect_tx(fb, static_cast<uint32_t>(ns * kABytes));
+                    for (int j = 0; j < ns; ++j)
+                        tma_load_4d(smem_u32(sA + (stage * kSub + j) * kABytes), mw, fb, (kb0 + j) * kBK, 0,
+                                    d.mt * (kWRows / 2), d.g);
+                    if (++stage == kStages) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+                if (!ok) break;
+                if (first) pdl_wait();   // the counter is cleared by then
+                first = false;
+            }
+            if (first) pdl_wait();
+        }
+    } else if (warp == 6) {
+        // ------------------------------------------------------------ token rows
+        if (lane == 0) {
+            pdl_wait();
+            int stage = 0;
+            uint32_t phase = 0;
+            Unit d;
+            while (next_unit(&d, false)) {
+                if (d.kind == kRound) continue;
+                const CUtensorMap* mx = d.kind == kFc1 ? &tmX : &tmA;
+                const int nk = d.kind == kFc1 ? nk1 : nk2;
+                if (d.kind == kFc2) {
+                    if (!wait_count(p.ready + d.chunk, d.nrows, abort_flag)) break;
+                    fence_proxy_async_global();
+                }
+                const int nl = (d.nrows + kBox - 1) / kBox;
+                bool ok = true;
+                for (int kb0 = 0; kb0 < nk; kb0 += kSub) {
+                    const int ns = min(kSub, nk - kb0);
+                    ok = mbar_wait(smem_u32(&empty[stage]), phase ^ 1u, abort_flag, kWaitNs);
+                    if (!ok) break;
+                    const uint32_t fb = smem_u32(&full[stage]);
+                    mbar_arrive_expect_tx(fb, static_cast<uint32_t>(ns * nl * kBox * kBK));
+                    for (int j = 0; j < ns; ++j)
+                        for (int i = 0; i < nl; ++i)
+                            tma_load_2d(smem_u32(sB + (stage * kSub + j) * kBBytes) + i * kBox * kBK, mx, fb,
+                                        (kb0 + j) * kBK, d.row0 + i * kBox);
+                    if (++stage == kStages) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+                if (!ok) break;
+            }
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ MMA issuer
+        if (lane == 0) {
+            int stage = 0, acc = 0;
+            uint32_t phase = 0, acc_phase = 0;
+            Unit d;
+            while (next_unit(&d, false)) {
+                if (d.kind == kRound) continue;
+                const int nk = d.kind == kFc1 ? nk1 : nk2, K = d.kind == kFc1 ? p.H : p.I;
+                const uint32_t idesc = idesc_s8_s32(kWRows, ((d.nrows + 15) / 16) * 16);
+                if (!mbar_wait(smem_u32(&tempty[acc]), acc_phase ^ 1u, abort_flag, kWaitNs)) break;
+                tc_fence_after();
+                const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * kTok);
+                bool ok = true;
+                for (int kb0 = 0; kb0 < nk; kb0 += kSub) {
+                    const int ns = min(kSub, nk - kb0);
+                    if (!mbar_wait(smem_u32(&full[stage]), phase, abort_flag, kWaitNs)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    for (int j = 0; j < ns; ++j) {
+                        const int sl = stage * kSub + j;
+                        const uint32_t a0 = smem_u32(sA + sl * kABytes), b0 = smem_u32(sB + sl * kBBytes);
+#pragma unroll
+                        for (int kk = 0; kk < kBK / 32; ++kk)
+                            if ((kb0 + j) * kBK + kk * 32 < K)   // nothing but zeros past K
+                                umma_s8(d_tmem, smem_desc_sw128(a0 + kk * 32), smem_desc_sw128(b0 + kk * 32), idesc,
+                                        (kb0 + j > 0 || kk > 0) ? 1u : 0u);
+                    }
+                    umma_commit(smem_u32(&empty[stage]));
+                    if (++stage == kStages) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+                if (!ok) break;
+                umma_commit(smem_u32(&tfull[acc]));
+                acc ^= 1;
+                if (acc == 0) acc_phase ^= 1u;
+            }
+        }
+    } else {
+        // ------------------------------------------------------------ epilogue
+        pdl_wait();
+        const int quad = warp & 3, r = quad * 32 + lane;
+        int acc = 0;
+        uint32_t acc_phase = 0;
+        Unit d;
+        while (next_unit(&d, true)) {
+            if (d.kind == kRound) {
+                // this warp's two rows, once the chunk's fc1 units have all been here
+                const int r0 = d.mt * kRoundRows + 2 * (warp - 2);
+                const int n = min(2, d.nrows - r0);
+                if (n <= 0) continue;
+                bool ok = true;
+                if (lane == 0) ok = wait_count(p.done + d.chunk, 4 * MT1, abort_flag);
+                if (!__shfl_sync(0xffffffffu, ok, 0)) break;
+                round_rows(p, d.row0 + r0, n == 2, lane);
+                fence_proxy_async_global();   // read by TMA
+                __threadfence();
+                __syncwarp();
+                if (lane == 0) atomicAdd(p.ready + d.chunk, n);
+                continue;
+            }
+            const bool f1 = d.kind == kFc1;
+            const int wr = d.mt * kWRows + r, n_out = f1 ? 2 * p.I : p.H;
+            const bool wvalid = wr < n_out;   // even counts: a (gate, up) pair is valid or not as one
+            float sw = 0.f, bias = 0.f;
+            if (wvalid) {
+                const size_t i = static_cast<size_t>(d.g) * n_out + (f1 ? fc1_row(wr, p.I, p.chunked) : wr);
+                const __nv_bfloat16* b = f1 ? p.b1 : p.b2;
+                sw = (f1 ? p.s1 : p.s2)[i];
+                if (b) bias = bf16_at(b, i);
+            }
+            const float* scales = f1 ? p.xs : p.as;
+            if (!mbar_wait(smem_u32(&tfull[acc]), acc_phase, abort_flag, kWaitNs)) break;
+            tc_fence_after();
+            const uint32_t tb = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + static_cast<uint32_t>(acc * kTok);
+#pragma unroll 1
+            for (int c = 0; c < d.nrows; c += 16) {
+                uint32_t v[16];
+                float sa[16];
+                tmem_ld_32x32b_x16(tb + c, v);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) sa[i] = __ldcg(scales + d.row0 + min(c + i, d.nrows - 1));
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const int n = c + i;
+                    const float x = fmaf(static_cast<float>(static_cast<int>(v[i])), sa[i] * sw, bias);
+                    if (f1) {
+                        const float up = __shfl_xor_sync(0xffffffffu, x, 1);
+                        if (!(lane & 1) && wvalid && n < d.nrows)
+                            p.act[static_cast<size_t>(d.row0 + n) * p.I + (wr >> 1)] = swiglu_attr_fast(x, up, p.attr);
+                    } else if (wvalid && n < d.nrows) {
+                        p.y[static_cast<size_t>(d.row0 + n) * p.H + wr] = __float2bfloat16_rn(x);
+                    }
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&tempty[acc]));
+            acc ^= 1;
+            if (acc == 0) acc_phase ^= 1u;
+            if (f1) {
+                __threadfence();
+                __syncwarp();
+                if (lane == 0) atomicAdd(p.done + d.chunk, 1);
+            }
+        }
+    }
+    if (*abort_flag) {
+        // copies already issued may still land: give them time before the CTA exits
+        const uint64_t t0 = global_timer_ns();
+        while (global_timer_ns() - t0 < 200000ull) __nanosleep(1000);
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem_base, 2 * kTok);
+    }
+    // errors: a wait that ran out, offsets out of order (found again for the report, behind
+    // pdl_wait; block 0)
+    if (threadIdx.x == 0) {
+        pdl_wait();
+        if (*abort_flag) atomicOr(p.err, kErrTimeout);
+    }
+    if (blockIdx.x == 0 && warp == 2) build_group_tiles(p.offsets, p.rows, p.err, p.E, kTok, s_off, s_pre, lane);
+}
+
+}  // namespace
+
+bool q8_ffn_supported(int rows, int E) { return static_cast<long long>(rows) <= static_cast<long long>(kTok) * E; }
+
+// Two words per chunk and the scheduler's.
+int q8_ffn_counters(int rows, int E) { return 2 * (rows / kTok + E + 1) + 1; }
+
+cudaError_t launch_q8_ffn(const Q8FfnArgs& a, cudaStream_t s) {
+    if (a.rows <= 0) return cudaSuccess;
+    CUtensorMap w1, x, w2, act;
+    if (!tmap::pairs8(&w1, a.fc1_q, a.E, 2 * a.I, a.H, kWRows / 2, a.ep.fc1_chunked)) return cudaErrorInvalidValue;
+    if (!tmap::pairs8(&w2, a.fc2_q, a.E, a.H, a.I, kWRows / 2, false)) return cudaErrorInvalidValue;
+    if (!tmap::matrix8(&x, a.x_q, a.rows, a.H, kBox)) return cudaErrorInvalidValue;
+    if (!tmap::matrix8(&act, a.act_q, a.rows, a.I, kBox)) return cudaErrorInvalidValue;
+    const int chunks = a.rows / kTok + a.E + 1;
+    const Params p{a.offsets, a.E, a.rows, a.H, a.I, a.x_scale, a.ep.fc1_scale, a.ep.fc2_scale,
+                   static_cast<const __nv_bfloat16*>(a.ep.fc1_bias), static_cast<const __nv_bfloat16*>(a.ep.fc2_bias),
+                   a.act, a.act_q, a.act_scale, static_cast<__nv_bfloat16*>(a.y), a.counters, a.counters + chunks,
+                   a.counters + 2 * chunks, a.err, a.ep.act, a.ep.fc1_chunked};
+    static bool done[64] = {false};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (!done[dev]) {
+        const cudaError_t e = cudaFuncSetAttribute(q8_ffn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+        if (e != cudaSuccess) return e;
+        done[dev] = true;
+    }
+    // chunks: at most one a row, and one per 64 rows and one more for every expert
+    const long long most = a.rows < a.rows / kTok + a.E ? a.rows : a.rows / kTok + a.E;
+    const long long units = most * ((2 * a.I + kWRows - 1) / kWRows + kRounds + (a.H + kWRows - 1) / kWRows);
+    const int sms = device_sm_count();
+    return launch_k_coop(q8_ffn_kernel, dim3(static_cast<unsigned>(units < sms ? units : sms)), dim3(kThreads),
+                         static_cast<size_t>(kSmemBytes), s, true, w1, x, w2, act, p);
+}
+
+}  // namespace moe

@@ -762,9 +762,9 @@ cudaError_t launch_pair(const CUtensorMap& w, const CUtensorMap& x, const Q8Para
 constexpr int kStreamRows = kSTok;
 
 template <int MODE>
-cudaError_t stream_product(const Q8GemmArgs& a, const Q8Params& p, bool chunked, cudaStream_t s) {
+cudaError_t stream_product(const Q8GemmArgs& a, const Q8Params& p, cudaStream_t s) {
     CUtensorMap w, x;
-    if (!tmap::pairs8(&w, a.w_q, a.E, a.N, a.K, kSWRows / 2, chunked)) return cudaErrorInvalidValue;
+    if (!tmap::pairs8(&w, a.w_q, a.E, a.N, a.K, kSWRows / 2, false)) return cudaErrorInvalidValue;
     if (!tmap::matrix8(&x, a.a_q, a.rows, a.K, kSBox)) return cudaErrorInvalidValue;
     // chunks: at most one per row, and one per 64 rows and one more for every expert
     // (dense: no more)
@@ -789,7 +789,9 @@ cudaError_t product(const Q8GemmArgs& a, const Q8Params& p, cudaStream_t s) {
                                 ((a.N + 2 * kPWRows - 1) / (2 * kPWRows));
         return launch_pair<MODE>(w, x, p, units, s);
     }
-    return stream_product<MODE>(a, p, chunked, s);
+    // fc1 alone runs here for many rows only (the FFN of few rows is one launch: ffn_q8.cu)
+    if constexpr (MODE == OUT_SWIGLU) return cudaErrorInvalidValue;
+    else return stream_product<MODE>(a, p, s);
 }
 }  // namespace
 

@@ -186,9 +186,10 @@ cudaError_t launch_ffn_pair(const void* x_perm, const int32_t* offsets, const vo
                             int32_t* err, cudaStream_t s, cudaEvent_t mid, const FfnAttrs& ep);
 
 // ---------------------------------------------------------------- quantize.cu
-// q [rows, K] int8 and scale [rows] of x [rows, K] (bf16 or float32; K a multiple of 8).
+// q [rows, K] int8 and scale [rows] of x [rows, K] (bf16 or float32; K a multiple of 8); the
+// same launch zeroes `clear_words` 32-bit words at `clear`.
 cudaError_t launch_quantize_rows(const void* x, int rows, int K, bool bf16, int8_t* q, float* scale,
-                                 cudaStream_t s);
+                                 cudaStream_t s, int32_t* clear = nullptr, int clear_words = 0);
 
 // ---------------------------------------------------------------- gemm_q8.cu
 // One grouped product of int8 rows and int8 weights (K a multiple of 16, N of 32).
@@ -208,6 +209,29 @@ struct Q8GemmArgs {
     int32_t* err = nullptr;            // device error word or nullptr
 };
 cudaError_t launch_q8_gemm(const Q8GemmArgs& a, cudaStream_t s);
+
+// ---------------------------------------------------------------- ffn_q8.cu
+// The whole int8 expert FFN for at most 64 rows per expert on average, from int8 rows.  Must
+// be launched directly behind launch_quantize_rows on the same stream (its first loads do not
+// wait for it, only for what lies before it).
+bool q8_ffn_supported(int rows, int E);
+int q8_ffn_counters(int rows, int E);   // int32 words it needs, zero on entry
+struct Q8FfnArgs {
+    const int8_t* x_q = nullptr;       // [rows, H]
+    const float* x_scale = nullptr;    // [rows]
+    const int32_t* offsets = nullptr;  // [E + 1]
+    const int8_t* fc1_q = nullptr;     // [E, 2I, H]
+    const int8_t* fc2_q = nullptr;     // [E, H, I]
+    int rows = 0, H = 0, E = 0, I = 0;
+    FfnAttrs ep;                       // attributes, layout, biases, weight scales
+    float* act = nullptr;              // [rows, I] scratch
+    int8_t* act_q = nullptr;           // [rows, I] scratch
+    float* act_scale = nullptr;        // [rows] scratch
+    int32_t* counters = nullptr;
+    int32_t* err = nullptr;
+    void* y = nullptr;                 // [rows, H] bf16
+};
+cudaError_t launch_q8_ffn(const Q8FfnArgs& a, cudaStream_t s);
 
 // ---------------------------------------------------------------- balance.cu
 size_t balance_workspace_bytes(int T, int E, int S);

@@ -67,11 +67,12 @@ struct Vec8 {
 template <bool BF16, int TPR, int kRegVec>
 __global__ void __launch_bounds__(kQThreads)
 quantize_rows_kernel(const void* __restrict__ x, int rows, int K, int8_t* __restrict__ q,
-                     float* __restrict__ scale) {
+                     float* __restrict__ scale, int32_t* __restrict__ clear, int clear_words) {
     constexpr int kRows = kQThreads / TPR;   // rows of a block
     __shared__ uint32_t s_max[kQThreads / 32];
     pdl_wait();
     pdl_trigger();
+    for (int i = blockIdx.x * kQThreads + threadIdx.x; i < clear_words; i += gridDim.x * kQThreads) clear[i] = 0;
     const int nvec = K / 8;
     const int t = threadIdx.x % TPR;
     const long long row = static_cast<long long>(blockIdx.x) * kRows + threadIdx.x / TPR;
@@ -140,12 +141,13 @@ quantize_rows_kernel(const void* __restrict__ x, int rows, int K, int8_t* __rest
 }
 
 template <bool BF16>
-cudaError_t launch(const void* x, int rows, int K, int8_t* q, float* scale, cudaStream_t s) {
+cudaError_t launch(const void* x, int rows, int K, int8_t* q, float* scale, cudaStream_t s, int32_t* clear,
+                   int clear_words) {
     const int nvec = K / 8;
     auto go = [&](auto kern, int tpr) {
         const int per = kQThreads / tpr;
         return launch_k(kern, dim3(static_cast<unsigned>((rows + per - 1) / per)), dim3(kQThreads), 0, s, x, rows, K, q,
-                        scale);
+                        scale, clear, clear_words);
     };
     // Many rows: as few threads a row as hold it in registers, for many loads in flight and
     // no barrier.  Few rows (less than four blocks an SM): spread a row, for latency.
@@ -166,9 +168,10 @@ cudaError_t launch(const void* x, int rows, int K, int8_t* q, float* scale, cuda
 }  // namespace
 
 cudaError_t launch_quantize_rows(const void* x, int rows, int K, bool bf16, int8_t* q, float* scale,
-                                 cudaStream_t s) {
+                                 cudaStream_t s, int32_t* clear, int clear_words) {
     if (rows <= 0) return cudaSuccess;
-    return bf16 ? launch<true>(x, rows, K, q, scale, s) : launch<false>(x, rows, K, q, scale, s);
+    return bf16 ? launch<true>(x, rows, K, q, scale, s, clear, clear_words)
+                : launch<false>(x, rows, K, q, scale, s, clear, clear_words);
 }
 
 }  // namespace moe

@@ -197,18 +197,19 @@ def _addr(t):
 
 
 _HERE = contextlib.nullcontext()
+_raw_stream = torch._C._cuda_getCurrentRawStream   # of a device: 0.1 us, a Stream object 3 us
 
 
 def _on(t, stream):
-    """(stream, context) of a call: the caller's stream, or the current one of t's device.
-    What is allocated inside the context belongs to that stream; the context is empty where
-    the stream is the current one already."""
+    """(stream handle, context) of a call: the caller's stream, or the current one of t's
+    device.  What is allocated inside the context belongs to that stream; the context is
+    empty where the stream is the current one already."""
     if stream is None:
-        s = torch.cuda.current_stream(t.device)
-        return s, (_HERE if t.device.index == torch.cuda.current_device() else torch.cuda.stream(s))
+        i = t.device.index
+        return _raw_stream(i), (_HERE if i == torch.cuda.current_device() else torch.cuda.device(i))
     if stream.device != t.device:
         raise ValueError(f"the stream is on {stream.device}, the tensors are on {t.device}")
-    return stream, torch.cuda.stream(stream)
+    return stream.cuda_stream, torch.cuda.stream(stream)
 
 
 def quantize_rows(x, q=None, scale=None, stream=None):
@@ -221,14 +222,14 @@ def quantize_rows(x, q=None, scale=None, stream=None):
     s, here = _on(x, stream)
     with here:
         if q is None:
-            q = torch.empty((rows, K), dtype=torch.int8, device=x.device)
+            q = torch.empty_like(x, dtype=torch.int8)
         if scale is None:
-            scale = torch.empty((rows,), dtype=torch.float32, device=x.device)
+            scale = x.new_empty((rows,), dtype=torch.float32)
         _need(q, "q", torch.int8, (rows, K))
         _need(scale, "scale", torch.float32, (rows,))
         _same_device(x, q, scale)
         check(_lib().moe_quantize_rows(_addr(x), rows, K, _dtcode(x), _addr(q), _addr(scale),
-                                       s.cuda_stream), "moe_quantize_rows")
+                                       s), "moe_quantize_rows")
     return q, scale
 
 
@@ -265,7 +266,7 @@ def matmul_q8(a_q, a_scale, w_q, w_scale, offsets=None, bias=None, out=None,
         _same_device(a_q, a_scale, w_q, w_scale, offsets, bias, out, err_word)
         check(_lib().moe_matmul_q8(_addr(a_q), _addr(a_scale), _addr(w_q), _addr(w_scale), _addr(bias),
                                    _addr(offsets), rows, K, E, N, dt, _addr(out), _addr(err_word),
-                                   s.cuda_stream), "moe_matmul_q8")
+                                   s), "moe_matmul_q8")
     return out
 
 
@@ -304,7 +305,7 @@ def expert_ffn_w8a8(x_perm, offsets, fc1_q, fc1_scale, fc2_q, fc2_scale, y_perm=
                                          _addr(fc2_q), _addr(fc2_scale), _addr(fc1_bias),
                                          _addr(fc2_bias), rows, H, E, I, _swiglu(*swiglu),
                                          _layout(fc1_layout), _addr(y_perm), _addr(workspace),
-                                         workspace.numel(), s.cuda_stream), "moe_expert_ffn_w8a8")
+                                         workspace.numel(), s), "moe_expert_ffn_w8a8")
     return y_perm
 
 
@@ -347,7 +348,7 @@ def forward_w8a8(hidden, router_w, fc1_q, fc1_scale, fc2_q, fc2_scale, k, normal
                                       _addr(fc1_scale), _addr(fc2_q), _addr(fc2_scale), _addr(fc1_bias),
                                       _addr(fc2_bias), T, H, E, k, I, int(bool(normalize)),
                                       _swiglu(*swiglu), _layout(fc1_layout), _addr(out),
-                                      _addr(workspace), workspace.numel(), s.cuda_stream),
+                                      _addr(workspace), workspace.numel(), s),
               "moe_forward_w8a8")
     return out
 
@@ -382,21 +383,19 @@ def balance_loss(logits, topk_idx, coef=1.0, mask=None, seq_offsets=None, err_wo
     if err_word is not None:
         _need(err_word, "err_word", torch.int32)
     s, here = _on(logits, stream)
-    dev = logits.device
     with here:
-        loss = torch.empty((1,), dtype=torch.float32, device=dev)
-        counts = torch.empty((S, E), dtype=torch.int32, device=dev)
-        probs = torch.empty((S, E), dtype=torch.float32, device=dev)
-        tokens = torch.empty((S,), dtype=torch.int32, device=dev)
+        loss, probs = logits.new_empty((1,)), logits.new_empty((S, E))
+        counts = logits.new_empty((S, E), dtype=torch.int32)
+        tokens = logits.new_empty((S,), dtype=torch.int32)
         if workspace is None:
-            workspace = torch.empty(max(_lib().moe_balance_loss_workspace_size(T, E, S), 256),
-                                    dtype=torch.uint8, device=dev)
+            workspace = logits.new_empty((max(_lib().moe_balance_loss_workspace_size(T, E, S), 256),),
+                                         dtype=torch.uint8)
         _need(workspace, "workspace", torch.uint8)
         _same_device(logits, topk_idx, mask, seq_offsets, err_word, workspace)
         check(_lib().moe_balance_loss(_addr(logits), _addr(topk_idx), _addr(mask), _addr(seq_offsets),
                                       T, E, topk_idx.shape[1], S, float(coef), _addr(loss),
                                       _addr(counts), _addr(probs), _addr(tokens), _addr(err_word),
-                                      _addr(workspace), workspace.numel(), s.cuda_stream),
+                                      _addr(workspace), workspace.numel(), s),
               "moe_balance_loss")
     return dict(loss=loss, counts=counts, probs=probs, tokens=tokens)
 
@@ -423,7 +422,7 @@ def balance_loss_backward(logits, k, counts, tokens, coef=1.0, mask=None, seq_of
         check(_lib().moe_balance_loss_backward(_addr(logits), _addr(mask), _addr(seq_offsets),
                                                _addr(counts), _addr(tokens), T, E, int(k), S,
                                                float(coef), _addr(grad_loss), _addr(dlogits),
-                                               s.cuda_stream), "moe_balance_loss_backward")
+                                               s), "moe_balance_loss_backward")
     return dlogits
 
 
