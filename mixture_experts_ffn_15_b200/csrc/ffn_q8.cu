@@ -105,37 +105,58 @@ __device__ __forceinline__ bool wait_count(const int32_t* ctr, int target, volat
 
 __device__ __forceinline__ void fence_proxy_async_global() { asm volatile("fence.proxy.async.global;" ::: "memory"); }
 
-// The int8 rows of activation rows row and row + 1 (if `two`), by one warp; a row is read
-// twice (its maximum, then its values), both times from L2.
+// The int8 rows of activation rows row and row + 1 (if `two`), by one warp.
 __device__ __forceinline__ void round_rows(const Params& p, int row, bool two, int lane) {
     const int nvec = p.I / 4;
     const float4* x0 = reinterpret_cast<const float4*>(p.act + static_cast<size_t>(row) * p.I);
     const float4* x1 = two ? x0 + nvec : x0;
-    uint32_t m0 = 0, m1 = 0;
+    uint32_t* out = reinterpret_cast<uint32_t*>(p.aq + static_cast<size_t>(row) * p.I);
     auto top = [](const float4& v) {
         return max(max(__float_as_uint(v.x) & 0x7fffffffu, __float_as_uint(v.y) & 0x7fffffffu),
                    max(__float_as_uint(v.z) & 0x7fffffffu, __float_as_uint(v.w) & 0x7fffffffu));
     };
-#pragma unroll 4
-    for (int v = lane; v < nvec; v += 32) {
-        m0 = max(m0, top(__ldcg(x0 + v)));
-        m1 = max(m1, top(__ldcg(x1 + v)));
-    }
-    const RowQuant q0 = row_quant(__reduce_max_sync(0xffffffffu, m0));
-    const RowQuant q1 = row_quant(__reduce_max_sync(0xffffffffu, m1));
-    uint32_t* out = reinterpret_cast<uint32_t*>(p.aq + static_cast<size_t>(row) * p.I);
-    float far = ordinary(q0) && ordinary(q1) ? 0.f : 1.f;
+    float far = 0.f;
     auto fast = [&](const float4& v, const RowQuant& q) {
         const uint32_t n[4] = {quantize_fast<true>(v.x, 1.f, q.inv, &far), quantize_fast<true>(v.y, 1.f, q.inv, &far),
                                quantize_fast<true>(v.z, 1.f, q.inv, &far), quantize_fast<true>(v.w, 1.f, q.inv, &far)};
         return pack_s8x4(n);
     };
+    // up to kHold vectors a lane stay in registers between the maximum and the rounding; the
+    // rest of a longer row is read again
+    constexpr int kHold = 8;
+    float4 h0[kHold], h1[kHold];
+    uint32_t m0 = 0, m1 = 0;
+#pragma unroll
+    for (int j = 0; j < kHold; ++j)
+        if (lane + 32 * j < nvec) {
+            h0[j] = __ldcg(x0 + lane + 32 * j);
+            h1[j] = __ldcg(x1 + lane + 32 * j);
+        }
+#pragma unroll
+    for (int j = 0; j < kHold; ++j)
+        if (lane + 32 * j < nvec) {
+            m0 = max(m0, top(h0[j]));
+            m1 = max(m1, top(h1[j]));
+        }
 #pragma unroll 4
-    for (int v = lane; v < nvec; v += 32) {
+    for (int v = lane + 32 * kHold; v < nvec; v += 32) {
+        m0 = max(m0, top(__ldcg(x0 + v)));
+        m1 = max(m1, top(__ldcg(x1 + v)));
+    }
+    const RowQuant q0 = row_quant(__reduce_max_sync(0xffffffffu, m0));
+    const RowQuant q1 = row_quant(__reduce_max_sync(0xffffffffu, m1));
+#pragma unroll
+    for (int j = 0; j < kHold; ++j)
+        if (lane + 32 * j < nvec) {
+            out[lane + 32 * j] = fast(h0[j], q0);
+            if (two) out[nvec + lane + 32 * j] = fast(h1[j], q1);
+        }
+#pragma unroll 4
+    for (int v = lane + 32 * kHold; v < nvec; v += 32) {
         out[v] = fast(__ldcg(x0 + v), q0);
         if (two) out[nvec + v] = fast(__ldcg(x1 + v), q1);
     }
-    if (!(far <= kSureDistance)) {   // this lane's values again, exactly
+    if (!ordinary(q0) || !ordinary(q1) || !(far <= kSureDistance)) {   // this lane's values again, exactly
         auto exact = [](const float4& v, const RowQuant& q) {
             const uint32_t n[4] = {quantize_exact(v.x, q.pre, q.inv, q.amax), quantize_exact(v.y, q.pre, q.inv, q.amax),
                                    quantize_exact(v.z, q.pre, q.inv, q.amax), quantize_exact(v.w, q.pre, q.inv, q.amax)};
@@ -239,11 +260,16 @@ q8_ffn_kernel(const __grid_constant__ CUtensorMap tmW1, const __grid_constant__ 
         if (lane == 0) {
             int stage = 0;
             uint32_t phase = 0;
-            bool first = true;
-            for (;;) {
-                if (!mbar_wait(smem_u32(&uempty[slot]), uphase ^ 1u, abort_flag, kWaitNs)) break;
-                int u = static_cast<int>(blockIdx.x);
-                if (!first) u = static_cast<int>(gridDim.x) + atomicAdd(p.sched, 1);
+            bool waited = false;
+            // the next claim is made while the current unit's loads go out: the counter's
+            // round trip (1 us) is half of what an fc2 unit's weights take
+            int u = static_cast<int>(blockIdx.x), u_next = 0;
+            auto claim = [&]() {
+                if (!waited) pdl_wait();   // the counter is cleared by then
+                waited = true;
+                u_next = static_cast<int>(gridDim.x) + atomicAdd(p.sched, 1);
+            };
+            for (;; u = u_next) {
                 Unit d;
                 d.kind = u >= U ? kNone : u < U1 ? kFc1 : u < U2 ? kRound : kFc2;
                 if (d.kind != kNone) {
@@ -255,24 +281,24 @@ q8_ffn_kernel(const __grid_constant__ CUtensorMap tmW1, const __grid_constant__ 
                     d.row0 = s_off[d.g] + (d.chunk - s_pre[d.g]) * kTok;
                     d.nrows = min(kTok, s_off[d.g + 1] - d.row0);
                     if (d.kind == kRound && d.mt * kRoundRows >= d.nrows) {
-                        // no such rows: claim the next
-                        if (first) pdl_wait();
-                        first = false;
+                        claim();   // no such rows
                         continue;
                     }
                 }
+                if (!mbar_wait(smem_u32(&uempty[slot]), uphase ^ 1u, abort_flag, kWaitNs)) break;
                 s_unit[slot] = d;
                 mbar_arrive(smem_u32(&ufull[slot]));
                 next_slot();
                 if (d.kind == kNone) break;
                 if (d.kind == kRound) {
-                    if (first) pdl_wait();
-                    first = false;
+                    claim();
                     continue;
                 }
                 // one load instruction for both weight tensors, its map chosen at run time
                 const CUtensorMap* mw = d.kind == kFc1 ? &tmW1 : &tmW2;
                 const int nk = d.kind == kFc1 ? nk1 : nk2;
+                // behind the first unit's first ring of loads, any other unit's first stage
+                const int claim_at = waited ? 0 : min((nk - 1) / kSub, kStages - 1) * kSub;
                 bool ok = true;
                 for (int kb0 = 0; kb0 < nk; kb0 += kSub) {
                     const int ns = min(kSub, nk - kb0);
@@ -287,12 +313,11 @@ q8_ffn_kernel(const __grid_constant__ CUtensorMap tmW1, const __grid_constant__ 
                         stage = 0;
                         phase ^= 1u;
                     }
+                    if (kb0 == claim_at) claim();
                 }
                 if (!ok) break;
-                if (first) pdl_wait();   // the counter is cleared by then
-                first = false;
             }
-            if (first) pdl_wait();
+            if (!waited) pdl_wait();
         }
     } else if (warp == 6) {
         // ------------------------------------------------------------ token rows
