@@ -4,12 +4,9 @@
 //
 // 128 weight rows on the MMA's M side, a chunk of up to 64 token rows of one expert on N, so
 // that every weight byte streams from HBM once; bound by that stream.  The unit list holds
-// every fc1 unit (chunk x 128 rows of fc1), then the rounding units (up to 8 rows of a chunk's
-// activations), then every fc2 unit.  A CTA's first unit is unit blockIdx.x, later ones come
-// in list order from a counter (starting at the grid size), so the long fc1 units go first
-// and the short fc2 units even out the end.  (The rounding by the one warp that completes a
-// chunk, without units of its own, took 576 us instead of @@ at 2048 rows: 64 rows are too
-// many for a warp.)
+// every fc1 unit (chunk x 128 rows of fc1), then every fc2 unit.  A CTA's first unit is unit
+// blockIdx.x, later ones come in list order from a counter (starting at the grid size), so
+// the long fc1 units go first and the short fc2 units even out the end.
 //
 // Warps of a CTA:
 //   0    claims the units and streams their weights (TMA) into the ring.  Weights depend on
@@ -17,10 +14,14 @@
 //        start before that kernel has finished, and those of an fc2 unit before its
 //        activations exist.
 //   1    issues the MMAs (tcgen05 kind::i8) into one of two accumulators
-//   2-5  epilogue.  fc1: the activations in float32 to scratch.  Rounding: two rows a warp,
-//        once every fc1 unit of the chunk has been here (a counter).  fc2: scales, bias,
-//        bf16 outputs.
+//   2-5  epilogue.  fc1: the activations in float32 to scratch, counted per chunk.  fc2:
+//        scales, bias, bf16 outputs.
 //   6    streams the token rows: x's, or a chunk's activations once they are published
+//   7    cuts activations to int8, two rows at a time, as soon as their chunk's count is
+//        complete.  Row pairs are strided over the CTAs, apart from the units: rounding as
+//        units of the list, taken by the epilogue in its turn, came up to 8 us late for the
+//        last chunks (32 rows: @@ us), and by the warp that completes a chunk it took 576 us
+//        at 2048 rows.
 // The launch is cooperative (every CTA resident), so a unit waited for is some running CTA's.
 // Every wait is bounded (2 s) and reports MOE_DEVERR_TIMEOUT.
 #include <cuda.h>
@@ -47,7 +48,7 @@ constexpr int kSlots = kStages * kSub;
 constexpr int kABytes = kWRows * kBK;
 constexpr int kBBytes = kTok * kBK;
 constexpr int kRing = 8;                 // claimed units handed to the other warps
-constexpr int kThreads = 224;
+constexpr int kThreads = 256;
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr int kMiscBytes = kRing * 32 + (2 * kStages + 4 + 2 * kRing) * 8 + 16 + 2 * (kMaxExperts + 1) * 4 + 64;
 constexpr int kSmemBytes = 1024 + kSlots * (kABytes + kBBytes) + kMiscBytes;
@@ -78,9 +79,7 @@ struct __align__(16) Unit {
     int chunk, kind;
     int pad[2];
 };
-enum Kind : int { kNone = -1, kFc2 = 0, kFc1 = 1, kRound = 2 };
-constexpr int kRoundRows = 8;            // rows of a rounding unit: two for each epilogue warp
-constexpr int kRounds = kTok / kRoundRows;
+enum Kind : int { kNone = -1, kFc2 = 0, kFc1 = 1 };
 
 __device__ __forceinline__ int ld_acquire(const int32_t* p) {
     int v;
@@ -93,7 +92,7 @@ __device__ __forceinline__ bool wait_count(const int32_t* ctr, int target, volat
     if (ld_acquire(ctr) >= target) return true;
     const uint64_t t0 = global_timer_ns();
     for (;;) {
-        __nanosleep(32);
+        __nanosleep(64);
         if (ld_acquire(ctr) >= target) return true;
         if (*abort) return false;
         if (global_timer_ns() - t0 > kWaitNs) {
@@ -234,7 +233,7 @@ q8_ffn_kernel(const __grid_constant__ CUtensorMap tmW1, const __grid_constant__ 
 
     const int MT1 = (2 * p.I + kWRows - 1) / kWRows, MT2 = (p.H + kWRows - 1) / kWRows;
     const int chunks = s_pre[p.E];
-    const int U1 = chunks * MT1, U2 = U1 + chunks * kRounds, U = U2 + chunks * MT2;
+    const int U1 = chunks * MT1, U = U1 + chunks * MT2;
     const int nk1 = (p.H + kBK - 1) / kBK, nk2 = (p.I + kBK - 1) / kBK;
 
     int slot = 0;
@@ -271,29 +270,20 @@ q8_ffn_kernel(const __grid_constant__ CUtensorMap tmW1, const __grid_constant__ 
             };
             for (;; u = u_next) {
                 Unit d;
-                d.kind = u >= U ? kNone : u < U1 ? kFc1 : u < U2 ? kRound : kFc2;
+                d.kind = u >= U ? kNone : u < U1 ? kFc1 : kFc2;
                 if (d.kind != kNone) {
-                    const int v = d.kind == kFc1 ? u : d.kind == kRound ? u - U1 : u - U2;
-                    const int MT = d.kind == kFc1 ? MT1 : d.kind == kRound ? kRounds : MT2;
+                    const int v = d.kind == kFc1 ? u : u - U1, MT = d.kind == kFc1 ? MT1 : MT2;
                     d.chunk = v / MT;
                     d.mt = v - d.chunk * MT;
                     d.g = tile_group(d.chunk, p.E, s_pre);
                     d.row0 = s_off[d.g] + (d.chunk - s_pre[d.g]) * kTok;
                     d.nrows = min(kTok, s_off[d.g + 1] - d.row0);
-                    if (d.kind == kRound && d.mt * kRoundRows >= d.nrows) {
-                        claim();   // no such rows
-                        continue;
-                    }
                 }
                 if (!mbar_wait(smem_u32(&uempty[slot]), uphase ^ 1u, abort_flag, kWaitNs)) break;
                 s_unit[slot] = d;
                 mbar_arrive(smem_u32(&ufull[slot]));
                 next_slot();
                 if (d.kind == kNone) break;
-                if (d.kind == kRound) {
-                    claim();
-                    continue;
-                }
                 // one load instruction for both weight tensors, its map chosen at run time
                 const CUtensorMap* mw = d.kind == kFc1 ? &tmW1 : &tmW2;
                 const int nk = d.kind == kFc1 ? nk1 : nk2;
@@ -327,7 +317,6 @@ q8_ffn_kernel(const __grid_constant__ CUtensorMap tmW1, const __grid_constant__ 
             uint32_t phase = 0;
             Unit d;
             while (next_unit(&d, false)) {
-                if (d.kind == kRound) continue;
                 const CUtensorMap* mx = d.kind == kFc1 ? &tmX : &tmA;
                 const int nk = d.kind == kFc1 ? nk1 : nk2;
                 if (d.kind == kFc2) {
@@ -361,7 +350,6 @@ q8_ffn_kernel(const __grid_constant__ CUtensorMap tmW1, const __grid_constant__ 
             uint32_t phase = 0, acc_phase = 0;
             Unit d;
             while (next_unit(&d, false)) {
-                if (d.kind == kRound) continue;
                 const int nk = d.kind == kFc1 ? nk1 : nk2, K = d.kind == kFc1 ? p.H : p.I;
                 const uint32_t idesc = idesc_s8_s32(kWRows, ((d.nrows + 15) / 16) * 16);
                 if (!mbar_wait(smem_u32(&tempty[acc]), acc_phase ^ 1u, abort_flag, kWaitNs)) break;
@@ -396,6 +384,25 @@ q8_ffn_kernel(const __grid_constant__ CUtensorMap tmW1, const __grid_constant__ 
                 if (acc == 0) acc_phase ^= 1u;
             }
         }
+    } else if (warp == 7) {
+        // ------------------------------------------------------------ activations to int8
+        pdl_wait();
+        constexpr int kPairs = kTok / 2;
+        for (int v = static_cast<int>(blockIdx.x); v < chunks * kPairs && !*abort_flag; v += static_cast<int>(gridDim.x)) {
+            const int chunk = v / kPairs, r0 = 2 * (v - chunk * kPairs);
+            const int g = tile_group(chunk, p.E, s_pre);
+            const int row0 = s_off[g] + (chunk - s_pre[g]) * kTok;
+            const int n = min(2, min(kTok, s_off[g + 1] - row0) - r0);
+            if (n <= 0) continue;
+            bool ok = true;
+            if (lane == 0) ok = wait_count(p.done + chunk, 4 * MT1, abort_flag);
+            if (!__shfl_sync(0xffffffffu, ok, 0)) break;
+            round_rows(p, row0 + r0, n == 2, lane);
+            fence_proxy_async_global();   // read by TMA
+            __threadfence();
+            __syncwarp();
+            if (lane == 0) atomicAdd(p.ready + chunk, n);
+        }
     } else {
         // ------------------------------------------------------------ epilogue
         pdl_wait();
@@ -404,21 +411,6 @@ q8_ffn_kernel(const __grid_constant__ CUtensorMap tmW1, const __grid_constant__ 
         uint32_t acc_phase = 0;
         Unit d;
         while (next_unit(&d, true)) {
-            if (d.kind == kRound) {
-                // this warp's two rows, once the chunk's fc1 units have all been here
-                const int r0 = d.mt * kRoundRows + 2 * (warp - 2);
-                const int n = min(2, d.nrows - r0);
-                if (n <= 0) continue;
-                bool ok = true;
-                if (lane == 0) ok = wait_count(p.done + d.chunk, 4 * MT1, abort_flag);
-                if (!__shfl_sync(0xffffffffu, ok, 0)) break;
-                round_rows(p, d.row0 + r0, n == 2, lane);
-                fence_proxy_async_global();   // read by TMA
-                __threadfence();
-                __syncwarp();
-                if (lane == 0) atomicAdd(p.ready + d.chunk, n);
-                continue;
-            }
             const bool f1 = d.kind == kFc1;
             const int wr = d.mt * kWRows + r, n_out = f1 ? 2 * p.I : p.H;
             const bool wvalid = wr < n_out;   // even counts: a (gate, up) pair is valid or not as one
@@ -515,7 +507,7 @@ cudaError_t launch_q8_ffn(const Q8FfnArgs& a, cudaStream_t s) {
     }
     // chunks: at most one a row, and one per 64 rows and one more for every expert
     const long long most = a.rows < a.rows / kTok + a.E ? a.rows : a.rows / kTok + a.E;
-    const long long units = most * ((2 * a.I + kWRows - 1) / kWRows + kRounds + (a.H + kWRows - 1) / kWRows);
+    const long long units = most * ((2 * a.I + kWRows - 1) / kWRows + (a.H + kWRows - 1) / kWRows);
     const int sms = device_sm_count();
     return launch_k_coop(q8_ffn_kernel, dim3(static_cast<unsigned>(units < sms ? units : sms)), dim3(kThreads),
                          static_cast<size_t>(kSmemBytes), s, true, w1, x, w2, act, p);
