@@ -17,7 +17,10 @@
 //   2-5  epilogue.  fc1: the activations in float32 to scratch, counted per chunk.  fc2:
 //        scales, bias, bf16 outputs.
 //   6    streams the token rows: x's, or a chunk's activations once they are published
-//   7    cuts activations to int8, two rows at a time, as soon as their chunk's count is
+//   7    brings each unit's channel scales and biases, and its rows' scales, into shared
+//        memory ahead of the epilogue (which waited 2.5 us a unit for them in turn, more
+//        than an fc2 unit's weights take)
+//   8-11 cut activations to int8, two rows at a time, as soon as their chunk's count is
 //        complete.  Row pairs are strided over the CTAs, apart from the units: rounding as
 //        units of the list, taken by the epilogue in its turn, came up to 8 us late for the
 //        last chunks (32 rows: @@ us), and by the warp that completes a chunk it took 576 us
@@ -48,9 +51,14 @@ constexpr int kSlots = kStages * kSub;
 constexpr int kABytes = kWRows * kBK;
 constexpr int kBBytes = kTok * kBK;
 constexpr int kRing = 8;                 // claimed units handed to the other warps
-constexpr int kThreads = 256;
+constexpr int kRoundWarps = 4;
+constexpr int kThreads = 32 * (8 + kRoundWarps);
 constexpr uint64_t kWaitNs = 2000000000ull;
-constexpr int kMiscBytes = kRing * 32 + (2 * kStages + 4 + 2 * kRing) * 8 + 16 + 2 * (kMaxExperts + 1) * 4 + 64;
+struct Scales {
+    float sw[kWRows], bias[kWRows], sa[kTok];
+};
+constexpr int kMiscBytes = kRing * (32 + static_cast<int>(sizeof(Scales))) + (2 * kStages + 4 + 3 * kRing) * 8 + 16 +
+                           2 * (kMaxExperts + 1) * 4 + 64;
 constexpr int kSmemBytes = 1024 + kSlots * (kABytes + kBBytes) + kMiscBytes;
 static_assert(kSmemBytes <= 227 * 1024, "shared memory");
 
@@ -182,13 +190,15 @@ q8_ffn_kernel(const __grid_constant__ CUtensorMap tmW1, const __grid_constant__ 
     uint8_t* sA = smem;
     uint8_t* sB = smem + kSlots * kABytes;
     Unit* s_unit = reinterpret_cast<Unit*>(sB + kSlots * kBBytes);   // [kRing]
-    uint64_t* full = reinterpret_cast<uint64_t*>(s_unit + kRing);
+    Scales* s_scales = reinterpret_cast<Scales*>(s_unit + kRing);    // [kRing]
+    uint64_t* full = reinterpret_cast<uint64_t*>(s_scales + kRing);
     uint64_t* empty = full + kStages;
     uint64_t* tfull = empty + kStages;
     uint64_t* tempty = tfull + 2;
     uint64_t* ufull = tempty + 2;
     uint64_t* uempty = ufull + kRing;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(uempty + kRing);
+    uint64_t* sfull = uempty + kRing;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sfull + kRing);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     int* s_off = reinterpret_cast<int*>(tmem_slot + 4);
     int* s_pre = s_off + (kMaxExperts + 1);
@@ -205,7 +215,8 @@ q8_ffn_kernel(const __grid_constant__ CUtensorMap tmW1, const __grid_constant__ 
         }
         for (int q = 0; q < kRing; ++q) {
             mbar_init(smem_u32(&ufull[q]), 1);
-            mbar_init(smem_u32(&uempty[q]), 6);  // MMA, tokens, 4 epilogue warps
+            mbar_init(smem_u32(&uempty[q]), 7);  // MMA, tokens, scales, 4 epilogue warps
+            mbar_init(smem_u32(&sfull[q]), 1);
         }
         *abort_flag = 0;
         fence_mbar_init();
@@ -244,12 +255,11 @@ q8_ffn_kernel(const __grid_constant__ CUtensorMap tmW1, const __grid_constant__ 
             uphase ^= 1u;
         }
     };
-    // the next claimed unit, as every warp but the claiming one reads it (one lane or all)
-    auto next_unit = [&](Unit* d, bool whole_warp) {
+    // the next claimed unit, as the MMA's and the tokens' lane read it
+    auto next_unit = [&](Unit* d) {
         if (!mbar_wait(smem_u32(&ufull[slot]), uphase, abort_flag, kWaitNs)) return false;
         *d = s_unit[slot];
-        if (whole_warp) __syncwarp();
-        if (!whole_warp || lane == 0) mbar_arrive(smem_u32(&uempty[slot]));
+        mbar_arrive(smem_u32(&uempty[slot]));
         next_slot();
         return d->kind != kNone;
     };
@@ -316,7 +326,7 @@ q8_ffn_kernel(const __grid_constant__ CUtensorMap tmW1, const __grid_constant__ 
             int stage = 0;
             uint32_t phase = 0;
             Unit d;
-            while (next_unit(&d, false)) {
+            while (next_unit(&d)) {
                 const CUtensorMap* mx = d.kind == kFc1 ? &tmX : &tmA;
                 const int nk = d.kind == kFc1 ? nk1 : nk2;
                 if (d.kind == kFc2) {
@@ -349,7 +359,7 @@ q8_ffn_kernel(const __grid_constant__ CUtensorMap tmW1, const __grid_constant__ 
             int stage = 0, acc = 0;
             uint32_t phase = 0, acc_phase = 0;
             Unit d;
-            while (next_unit(&d, false)) {
+            while (next_unit(&d)) {
                 const int nk = d.kind == kFc1 ? nk1 : nk2, K = d.kind == kFc1 ? p.H : p.I;
                 const uint32_t idesc = idesc_s8_s32(kWRows, ((d.nrows + 15) / 16) * 16);
                 if (!mbar_wait(smem_u32(&tempty[acc]), acc_phase ^ 1u, abort_flag, kWaitNs)) break;
@@ -385,10 +395,56 @@ q8_ffn_kernel(const __grid_constant__ CUtensorMap tmW1, const __grid_constant__ 
             }
         }
     } else if (warp == 7) {
+        // ------------------------------------------------------------ scales
+        pdl_wait();
+        for (;;) {
+            const int at = slot;
+            if (!mbar_wait(smem_u32(&ufull[at]), uphase, abort_flag, kWaitNs)) break;
+            const Unit d = s_unit[at];
+            if (d.kind == kNone) break;
+            const bool f1 = d.kind == kFc1;
+            const int n_out = f1 ? 2 * p.I : p.H;
+            const float* s = f1 ? p.s1 : p.s2;
+            const __nv_bfloat16* b = f1 ? p.b1 : p.b2;
+            float sw[kWRows / 32], bias[kWRows / 32];
+#pragma unroll
+            for (int i = 0; i < kWRows / 32; ++i) {
+                const int wr = d.mt * kWRows + 32 * i + lane;
+                sw[i] = bias[i] = 0.f;
+                if (wr < n_out) {
+                    const size_t j = static_cast<size_t>(d.g) * n_out + (f1 ? fc1_row(wr, p.I, p.chunked) : wr);
+                    sw[i] = s[j];
+                    if (b) bias[i] = bf16_at(b, j);
+                }
+            }
+            if (!f1) {
+                bool ok = true;
+                if (lane == 0) ok = wait_count(p.ready + d.chunk, d.nrows, abort_flag);
+                if (!__shfl_sync(0xffffffffu, ok, 0)) break;
+            }
+            Scales& sc = s_scales[at];
+#pragma unroll
+            for (int i = 0; i < kTok / 32; ++i)
+                if (lane + 32 * i < d.nrows) sc.sa[lane + 32 * i] = __ldcg((f1 ? p.xs : p.as) + d.row0 + lane + 32 * i);
+#pragma unroll
+            for (int i = 0; i < kWRows / 32; ++i) {
+                sc.sw[32 * i + lane] = sw[i];
+                sc.bias[32 * i + lane] = bias[i];
+            }
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(smem_u32(&sfull[at]));
+                mbar_arrive(smem_u32(&uempty[at]));
+            }
+            next_slot();
+        }
+    } else if (warp >= 8) {
         // ------------------------------------------------------------ activations to int8
         pdl_wait();
         constexpr int kPairs = kTok / 2;
-        for (int v = static_cast<int>(blockIdx.x); v < chunks * kPairs && !*abort_flag; v += static_cast<int>(gridDim.x)) {
+        // neighbouring pairs on different CTAs: a chunk's rows are rounded at once
+        const int w0 = (warp - 8) * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x);
+        for (int v = w0; v < chunks * kPairs && !*abort_flag; v += kRoundWarps * static_cast<int>(gridDim.x)) {
             const int chunk = v / kPairs, r0 = 2 * (v - chunk * kPairs);
             const int g = tile_group(chunk, p.E, s_pre);
             const int row0 = s_off[g] + (chunk - s_pre[g]) * kTok;
@@ -409,34 +465,29 @@ q8_ffn_kernel(const __grid_constant__ CUtensorMap tmW1, const __grid_constant__ 
         const int quad = warp & 3, r = quad * 32 + lane;
         int acc = 0;
         uint32_t acc_phase = 0;
-        Unit d;
-        while (next_unit(&d, true)) {
+        for (;;) {
+            const int at = slot;
+            if (!mbar_wait(smem_u32(&ufull[at]), uphase, abort_flag, kWaitNs)) break;
+            const Unit d = s_unit[at];
+            if (d.kind == kNone) break;
             const bool f1 = d.kind == kFc1;
-            const int wr = d.mt * kWRows + r, n_out = f1 ? 2 * p.I : p.H;
-            const bool wvalid = wr < n_out;   // even counts: a (gate, up) pair is valid or not as one
-            float sw = 0.f, bias = 0.f;
-            if (wvalid) {
-                const size_t i = static_cast<size_t>(d.g) * n_out + (f1 ? fc1_row(wr, p.I, p.chunked) : wr);
-                const __nv_bfloat16* b = f1 ? p.b1 : p.b2;
-                sw = (f1 ? p.s1 : p.s2)[i];
-                if (b) bias = bf16_at(b, i);
-            }
-            const float* scales = f1 ? p.xs : p.as;
+            const int wr = d.mt * kWRows + r;
+            const bool wvalid = wr < (f1 ? 2 * p.I : p.H);   // even: a (gate, up) pair is valid or not as one
+            if (!mbar_wait(smem_u32(&sfull[at]), uphase, abort_flag, kWaitNs)) break;
+            const Scales& sc = s_scales[at];
+            const float sw = sc.sw[r], bias = sc.bias[r];
             if (!mbar_wait(smem_u32(&tfull[acc]), acc_phase, abort_flag, kWaitNs)) break;
             tc_fence_after();
             const uint32_t tb = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + static_cast<uint32_t>(acc * kTok);
 #pragma unroll 1
             for (int c = 0; c < d.nrows; c += 16) {
                 uint32_t v[16];
-                float sa[16];
                 tmem_ld_32x32b_x16(tb + c, v);
-#pragma unroll
-                for (int i = 0; i < 16; ++i) sa[i] = __ldcg(scales + d.row0 + min(c + i, d.nrows - 1));
                 tmem_wait_ld();
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                    const int n = c + i;
-                    const float x = fmaf(static_cast<float>(static_cast<int>(v[i])), sa[i] * sw, bias);
+                    const int n = c + i;   // past the chunk: a stale scale, nothing stored
+                    const float x = fmaf(static_cast<float>(static_cast<int>(v[i])), sc.sa[n] * sw, bias);
                     if (f1) {
                         const float up = __shfl_xor_sync(0xffffffffu, x, 1);
                         if (!(lane & 1) && wvalid && n < d.nrows)
@@ -447,15 +498,16 @@ q8_ffn_kernel(const __grid_constant__ CUtensorMap tmW1, const __grid_constant__ 
                 }
             }
             tc_fence_before();
+            if (f1) __threadfence();
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&tempty[acc]));
+            if (lane == 0) {
+                mbar_arrive(smem_u32(&tempty[acc]));
+                mbar_arrive(smem_u32(&uempty[at]));
+                if (f1) atomicAdd(p.done + d.chunk, 1);
+            }
             acc ^= 1;
             if (acc == 0) acc_phase ^= 1u;
-            if (f1) {
-                __threadfence();
-                __syncwarp();
-                if (lane == 0) atomicAdd(p.done + d.chunk, 1);
-            }
+            next_slot();
         }
     }
     if (*abort_flag) {

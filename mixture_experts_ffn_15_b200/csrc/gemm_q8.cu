@@ -250,7 +250,12 @@ q8_stream_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
 #pragma unroll 1
             for (int c = 0; c < nrows; c += 16) {
                 uint32_t v[16];
+                float sa[16];
                 tmem_ld_32x32b_x16(tb + c, v);
+                if constexpr (!SPLIT) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) sa[i] = __ldg(p.sa + row0 + min(c + i, nrows - 1));
+                }
                 tmem_wait_ld();
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
@@ -261,8 +266,7 @@ q8_stream_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
                         if (n < nrows)
                             st_shared_cluster_s32(mapa_shared(at, static_cast<uint32_t>(dst)), static_cast<int>(v[i]));
                     } else {
-                        const float sa = p.sa[row0 + min(n, nrows - 1)];
-                        const float y = fmaf(static_cast<float>(static_cast<int>(v[i])), sa * sw, bias);
+                        const float y = fmaf(static_cast<float>(static_cast<int>(v[i])), sa[i] * sw, bias);
                         store_one<MODE>(p, row0 + n, wr, y, n < nrows && wvalid);
                     }
                 }
@@ -284,10 +288,16 @@ q8_stream_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
             const bool wvalid = wr < p.N;
             float sw = 0.f, bias = 0.f;
             if (wvalid) channel<MODE>(p, g, wr, &sw, &bias);
-            for (int n = rank * per; n < min((rank + 1) * per, nrows); ++n) {
+            // the scales of the CTA's tokens (at most 32) ahead of the sums: a load a token in
+            // turn took 16 us at 61 rows
+            const int n0 = rank * per, n1 = min(n0 + per, nrows);
+            const float sa_lane = n0 + lane < n1 ? p.sa[row0 + n0 + lane] : 0.f;
+#pragma unroll 4
+            for (int n = n0; n < n1; ++n) {
                 int sum = 0;
-                for (int q = 0; q < cs; ++q) sum += s_part[(q * per + n - rank * per) * kSWRows + r];
-                store_one<MODE>(p, row0 + n, wr, fmaf(static_cast<float>(sum), p.sa[row0 + n] * sw, bias), wvalid);
+                for (int q = 0; q < cs; ++q) sum += s_part[(q * per + n - n0) * kSWRows + r];
+                const float sa = __shfl_sync(0xffffffffu, sa_lane, n - n0);
+                store_one<MODE>(p, row0 + n, wr, fmaf(static_cast<float>(sum), sa * sw, bias), wvalid);
             }
         }
     }
