@@ -87,7 +87,9 @@ __host__ __device__ constexpr int stream_slots(bool split) { return kSSub * (spl
 constexpr int kSABytes = kSWRows * kBK;
 constexpr int kSBBytes = kSTok * kBK;
 constexpr int kSThreads = 192;
-constexpr int kSPartBytes = kSWRows * kSTok * 4;   // partial sums of one unit (CS > 1)
+// partial sums of one unit (cs > 1): for each source CTA and weight row the 64 / cs tokens of
+// this CTA, rows padded by 16 bytes against bank conflicts (cs = 8: 8 x 128 x 12 words)
+constexpr int kSPartBytes = 8 * kSWRows * (kSTok / 8 + 4) * 4;
 constexpr int kSMiscBytes = (2 * kSMaxStages + 4) * 8 + 16 + 2 * (kMaxExperts + 1) * 4 + 64;
 
 constexpr int stream_smem(bool split) {
@@ -234,6 +236,7 @@ q8_stream_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
         }
     }
     const int quad = warp & 3, r = quad * 32 + lane;
+    const int per_log2 = 31 - __clz(kSTok / cs), per = 1 << per_log2;   // tokens a CTA of the cluster finishes
     if (warp >= 2) {
         int acc = 0;
         uint32_t acc_phase = 0;
@@ -257,15 +260,21 @@ q8_stream_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
                     for (int i = 0; i < 16; ++i) sa[i] = __ldg(p.sa + row0 + min(c + i, nrows - 1));
                 }
                 tmem_wait_ld();
+                if constexpr (SPLIT) {
+                    // four tokens of a weight row at a time, to the CTA that finishes them
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const int n = c + i;
-                    if constexpr (SPLIT) {
-                        const int per = kSTok / cs, dst = n / per;
-                        const uint32_t at = smem_u32(s_part + (rank * per + n - dst * per) * kSWRows + r);
+                    for (int i = 0; i < 16; i += 4) {
+                        const int n = c + i, dst = n >> per_log2;
                         if (n < nrows)
-                            st_shared_cluster_s32(mapa_shared(at, static_cast<uint32_t>(dst)), static_cast<int>(v[i]));
-                    } else {
+                            st_shared_cluster_v4(mapa_shared(smem_u32(s_part + (rank * kSWRows + r) * (per + 4) + n - (dst << per_log2)),
+                                                             static_cast<uint32_t>(dst)),
+                                                 __uint_as_float(v[i]), __uint_as_float(v[i + 1]), __uint_as_float(v[i + 2]),
+                                                 __uint_as_float(v[i + 3]));
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const int n = c + i;
                         const float y = fmaf(static_cast<float>(static_cast<int>(v[i])), sa[i] * sw, bias);
                         store_one<MODE>(p, row0 + n, wr, y, n < nrows && wvalid);
                     }
@@ -280,24 +289,30 @@ q8_stream_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
     }
     if constexpr (SPLIT) {
         __syncwarp();
-        cluster_sync();   // every partial sum of the cluster's unit has arrived
-        if (warp >= 2 && first < units) {
-            int g, row0, nrows;
-            const int mt = unit(first, &g, &row0, &nrows);
-            const int wr = mt * kSWRows + r, per = kSTok / cs;
-            const bool wvalid = wr < p.N;
-            float sw = 0.f, bias = 0.f;
+        // the finishing CTA's channel and token scales (at most 32 tokens), behind the barrier
+        int g = 0, row0 = 0, nrows = 0, mt = 0;
+        if (warp >= 2 && first < units) mt = unit(first, &g, &row0, &nrows);
+        const int wr = mt * kSWRows + r, n0 = rank * per, n1 = min(n0 + per, nrows);
+        const bool wvalid = wr < p.N;
+        float sw = 0.f, bias = 0.f, sa_lane = 0.f;
+        if (n0 < n1) {
             if (wvalid) channel<MODE>(p, g, wr, &sw, &bias);
-            // the scales of the CTA's tokens (at most 32) ahead of the sums: a load a token in
-            // turn took 16 us at 61 rows
-            const int n0 = rank * per, n1 = min(n0 + per, nrows);
-            const float sa_lane = n0 + lane < n1 ? p.sa[row0 + n0 + lane] : 0.f;
-#pragma unroll 4
-            for (int n = n0; n < n1; ++n) {
-                int sum = 0;
-                for (int q = 0; q < cs; ++q) sum += s_part[(q * per + n - n0) * kSWRows + r];
-                const float sa = __shfl_sync(0xffffffffu, sa_lane, n - n0);
-                store_one<MODE>(p, row0 + n, wr, fmaf(static_cast<float>(sum), sa * sw, bias), wvalid);
+            if (n0 + lane < n1) sa_lane = p.sa[row0 + n0 + lane];
+        }
+        cluster_sync();   // every partial sum of the cluster's unit has arrived
+        for (int n = n0; n < n1; n += 4) {
+            int sum[4] = {0, 0, 0, 0};
+            for (int q = 0; q < cs; ++q) {
+                const int4 v = *reinterpret_cast<const int4*>(s_part + (q * kSWRows + r) * (per + 4) + n - n0);
+                sum[0] += v.x;
+                sum[1] += v.y;
+                sum[2] += v.z;
+                sum[3] += v.w;
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float sa = __shfl_sync(0xffffffffu, sa_lane, (n - n0 + i) & 31);
+                store_one<MODE>(p, row0 + n + i, wr, fmaf(static_cast<float>(sum[i]), sa * sw, bias), wvalid && n + i < n1);
             }
         }
     }

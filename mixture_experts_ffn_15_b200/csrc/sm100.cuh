@@ -298,9 +298,6 @@ __device__ __forceinline__ void st_shared_cluster_v4(uint32_t cluster_addr, floa
                  : "memory");
 }
 
-__device__ __forceinline__ void st_shared_cluster_s32(uint32_t cluster_addr, int v) {
-    asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(cluster_addr), "r"(v) : "memory");
-}
 
 // Arrive on an mbarrier that may live in the other CTA of the cluster.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
