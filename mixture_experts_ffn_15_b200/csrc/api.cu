@@ -139,7 +139,7 @@ W8a8Layout w8a8_layout(int rows, int H, int E, int I) {
     Carver c;
     W8a8Layout L;
     L.err = c.take(kAlign);
-    L.counters = c.take(q8_ffn_supported(rows, E) ? static_cast<size_t>(q8_ffn_counters(rows, E)) * 4 : 0);
+    L.counters = c.take(q8_ffn_supported(rows, E, I) ? static_cast<size_t>(q8_ffn_counters(rows, E)) * 4 : 0);
     L.clear_end = c.off;
     L.xq = c.take(r * H);
     L.xs = c.take(r * 4);
@@ -792,7 +792,7 @@ static moe_status w8a8_ffn(const void* x_perm, const int32_t* offsets, const int
     float* as = reinterpret_cast<float*>(ws + L.as);
     MOE_CUDA(launch_quantize_rows(x_perm, rows, H, true, xq, xs, s, reinterpret_cast<int32_t*>(ws + L.err),
                                   static_cast<int>((L.clear_end - L.err) / 4)));
-    if (q8_ffn_supported(rows, E)) {
+    if (q8_ffn_supported(rows, E, I)) {
         Q8FfnArgs f;
         f.x_q = xq;
         f.x_scale = xs;

@@ -532,7 +532,18 @@ q8_ffn_kernel(const __grid_constant__ CUtensorMap tmW1, const __grid_constant__ 
 
 }  // namespace
 
-bool q8_ffn_supported(int rows, int E) { return static_cast<long long>(rows) <= static_cast<long long>(kTok) * E; }
+// One launch for up to 48 rows per expert on average; with 8 rows and more, only where fc1 has
+// more than two rounds of units for the CTA pairs (E ceil(2I / 256) > 148), since the separate
+// kernels (row quantiser, fc1, row quantiser, fc2) then have no stream to lose between them
+// and shorter waits.  Measured (one launch / separate, us): E = 128, H = 2816, I = 704: 32
+// rows 41.8 / 54.3, 1024 rows 127.0 / 158.1, 48 rows per expert 180.7 / 186.1, 64 per expert
+// 239.0 / 193.7; E = 32, H = 1024, I = 512 (128 units): 4 rows per expert 24.7 / 24.9, 32 per
+// expert 37.2 / 26.8; E = 8, H = 2816, I = 704: 1 row per expert 24.9 / 25.1, 32 per expert
+// 35.2 / 29.3.
+bool q8_ffn_supported(int rows, int E, int I) {
+    const long long r = rows;
+    return r <= 48LL * E && (r < 8LL * E || static_cast<long long>(E) * ((2 * I + 255) / 256) > 148);
+}
 
 // Two words per chunk and the scheduler's.
 int q8_ffn_counters(int rows, int E) { return 2 * (rows / kTok + E + 1) + 1; }

@@ -783,19 +783,32 @@ cudaError_t launch_pair(const CUtensorMap& w, const CUtensorMap& x, const Q8Para
     return launch_clusters(q8_pair_kernel<MODE>, 2 * pairs, 2, kPThreads, kPSmemBytes, s, w, x, p);
 }
 
-// Rows per expert up to which the streaming kernel runs (a chunk of it).
-constexpr int kStreamRows = kSTok;
+// The streaming kernel runs for up to 56 rows per expert on average, and wherever its units
+// fit on the GPU at once.  Measured (stream / pair, us): grouped, E = 128, 2816 -> 1408, 48
+// rows per expert 88.2 / 96.8, 64 rows 100.8 / 98.1, 128 rows 162.6 / 108.8; dense, 2816 ->
+// 1408, 128 rows 8.8 / 12.7, 768 rows (132 units) 12.1 / 14.0, 1024 rows (176) 18.1 / 14.0;
+// 4096 -> 4096, 256 rows (128 units) 14.6 / 17.3, 384 rows (192) 23.4 / 17.4.
+constexpr int kStreamRows = 56;
+
+// Upper bound of the 64-row chunks: one per 64 rows, one more for every expert, at most one a
+// row (dense: exactly one per 64 rows).
+long long stream_units(const Q8GemmArgs& a) {
+    long long chunks = (a.rows + kSTok - 1) / kSTok;
+    if (a.offsets) chunks = a.rows < chunks + a.E ? a.rows : chunks + a.E;
+    return chunks * ((a.N + kSWRows - 1) / kSWRows);
+}
+
+bool use_stream(const Q8GemmArgs& a) {
+    return static_cast<long long>(a.rows) <= static_cast<long long>(kStreamRows) * a.E ||
+           stream_units(a) <= device_sm_count();
+}
 
 template <int MODE>
 cudaError_t stream_product(const Q8GemmArgs& a, const Q8Params& p, cudaStream_t s) {
     CUtensorMap w, x;
     if (!tmap::pairs8(&w, a.w_q, a.E, a.N, a.K, kSWRows / 2, false)) return cudaErrorInvalidValue;
     if (!tmap::matrix8(&x, a.a_q, a.rows, a.K, kSBox)) return cudaErrorInvalidValue;
-    // chunks: at most one per row, and one per 64 rows and one more for every expert
-    // (dense: no more)
-    long long chunks = (a.rows + kSTok - 1) / kSTok;
-    if (a.offsets) chunks = a.rows < chunks + a.E ? a.rows : chunks + a.E;
-    const long long units = chunks * ((a.N + kSWRows - 1) / kSWRows);
+    const long long units = stream_units(a);
     const int sms = device_sm_count(), nk = (a.K + kBK - 1) / kBK;
     int cs = 8;
     while (cs > 1 && (units * cs > sms || cs > nk)) cs /= 2;
@@ -807,14 +820,14 @@ template <int MODE>
 cudaError_t product(const Q8GemmArgs& a, const Q8Params& p, cudaStream_t s) {
     CUtensorMap w, x;
     const bool chunked = a.swiglu && a.fc1_chunked;
-    if (static_cast<long long>(a.rows) > static_cast<long long>(kStreamRows) * a.E) {
+    if (MODE == OUT_SWIGLU || !use_stream(a)) {
         if (!tmap::quads8(&w, a.w_q, a.E, a.N, a.K, chunked)) return cudaErrorInvalidValue;
         if (!tmap::matrix8(&x, a.a_q, a.rows, a.K, kPBox)) return cudaErrorInvalidValue;
         const long long units = (static_cast<long long>((a.rows + kPTok - 1) / kPTok) + a.E) *
                                 ((a.N + 2 * kPWRows - 1) / (2 * kPWRows));
         return launch_pair<MODE>(w, x, p, units, s);
     }
-    // fc1 alone runs here for many rows only (the FFN of few rows is one launch: ffn_q8.cu)
+    // (fc1 alone has many rows: the FFN of few is one launch, ffn_q8.cu)
     if constexpr (MODE == OUT_SWIGLU) return cudaErrorInvalidValue;
     else return stream_product<MODE>(a, p, s);
 }

@@ -211,10 +211,10 @@ struct Q8GemmArgs {
 cudaError_t launch_q8_gemm(const Q8GemmArgs& a, cudaStream_t s);
 
 // ---------------------------------------------------------------- ffn_q8.cu
-// The whole int8 expert FFN for at most 64 rows per expert on average, from int8 rows.  Must
+// The whole int8 expert FFN in one launch, for few rows per expert, from int8 rows.  Must
 // be launched directly behind launch_quantize_rows on the same stream (its first loads do not
 // wait for it, only for what lies before it).
-bool q8_ffn_supported(int rows, int E);
+bool q8_ffn_supported(int rows, int E, int I);
 int q8_ffn_counters(int rows, int E);   // int32 words it needs, zero on entry
 struct Q8FfnArgs {
     const int8_t* x_q = nullptr;       // [rows, H]
