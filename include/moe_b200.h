@@ -324,7 +324,7 @@ moe_status moe_forward_w8a8(const void* hidden, const void* norm_weight, float n
  * A sequence without valid tokens adds 0.  Balanced experts give coef.
  *   logits      [T, E] float32 (moe_route's), topk_idx [T, k] int32 (moe_route's)
  *   mask        [T] bytes or NULL: 0 marks a token (padding) that takes no part; its
- *               logits and ids are not read
+ *               logits and ids have no effect, whatever they hold
  *   seq_offsets [S+1] int32 (device) or NULL: tokens seq_offsets[s] .. seq_offsets[s+1]-1
  *               are sequence s; non-decreasing, seq_offsets[0] = 0, seq_offsets[S] <= T;
  *               tokens behind the last sequence take no part

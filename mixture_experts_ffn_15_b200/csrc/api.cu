@@ -151,9 +151,9 @@ W8a8Layout w8a8_layout(int rows, int H, int E, int I) {
 }
 
 // Workspace of the layer with int8 experts: the routing's blocks (header and tile counts
-// first, cleared by one launch), the permuted rows, the FFN's workspace, its output.
+// first, cleared by one launch), the FFN's output and workspace.
 struct W8a8FwdLayout {
-    size_t tile_counts, logits, idx, w, near, counts, offsets, perm_src, perm_dst, x_perm, y, xn, ffn, total;
+    size_t tile_counts, logits, idx, w, near, counts, offsets, perm_src, perm_dst, y, xn, ffn, total;
 };
 
 W8a8FwdLayout w8a8_fwd_layout(int T, int H, int E, int k, int I) {
@@ -170,7 +170,6 @@ W8a8FwdLayout w8a8_fwd_layout(int T, int H, int E, int k, int I) {
     L.offsets = c.take(static_cast<size_t>(E + 1) * 4);
     L.perm_src = c.take(rows * 4);
     L.perm_dst = c.take(rows * 4);
-    L.x_perm = c.take(rows * H * 2);
     L.y = c.take(rows * H * 2);
     L.xn = c.take(t * H * 2);   // the normalised input (pre-FFN norm)
     L.ffn = c.take(w8a8_layout(static_cast<int>(rows), H, E, I).total);
@@ -739,7 +738,14 @@ moe_status moe_quantize_rows(const void* x, int rows, int K, moe_dtype dt, int8_
     if (rows == 0) return MOE_OK;
     if (!x || !q || !scale || !aligned(x, 16) || !aligned(q, 16) || !aligned(scale, 4))
         return MOE_ERR_INVALID_ARG;
-    MOE_CUDA(launch_quantize_rows(x, rows, K, dt == MOE_BF16, q, scale, static_cast<cudaStream_t>(stream)));
+    QuantizeArgs a;
+    a.x = x;
+    a.rows = rows;
+    a.K = K;
+    a.bf16 = dt == MOE_BF16;
+    a.q = q;
+    a.scale = scale;
+    MOE_CUDA(launch_quantize_rows(a, static_cast<cudaStream_t>(stream)));
     return MOE_OK;
 }
 
@@ -779,9 +785,10 @@ size_t moe_expert_ffn_w8a8_workspace_size(int rows, int H, int E, int I) {
     return w8a8_layout(rows, H, E, I).total;
 }
 
-// The int8 expert FFN of valid arguments.  Clears the start of its workspace; `err` may be
-// another word, cleared by the caller.
-static moe_status w8a8_ffn(const void* x_perm, const int32_t* offsets, const int8_t* fc1_q,
+// The int8 expert FFN of valid arguments, on the rows of x (x_perm; with perm_dst, hidden
+// [T, H], whose row t becomes the permuted rows perm_dst[t, :]).  Clears the start of its
+// workspace; `err` may be another word, cleared by the caller.
+static moe_status w8a8_ffn(const void* x, const int32_t* perm_dst, int T, int k, const int32_t* offsets, const int8_t* fc1_q,
                            const float* fc1_scale, const int8_t* fc2_q, const float* fc2_scale, int rows,
                            int H, int E, int I, const FfnAttrs& ep, void* y_perm, char* ws,
                            const W8a8Layout& L, int32_t* err, cudaStream_t s, cudaEvent_t mid) {
@@ -790,8 +797,18 @@ static moe_status w8a8_ffn(const void* x_perm, const int32_t* offsets, const int
     float* act = reinterpret_cast<float*>(ws + L.act);
     int8_t* aq = reinterpret_cast<int8_t*>(ws + L.aq);
     float* as = reinterpret_cast<float*>(ws + L.as);
-    MOE_CUDA(launch_quantize_rows(x_perm, rows, H, true, xq, xs, s, reinterpret_cast<int32_t*>(ws + L.err),
-                                  static_cast<int>((L.clear_end - L.err) / 4)));
+    QuantizeArgs q;
+    q.x = x;
+    q.rows = perm_dst ? T : rows;
+    q.K = H;
+    q.q = xq;
+    q.scale = xs;
+    q.perm_dst = perm_dst;
+    q.k = k;
+    q.rows_out = rows;
+    q.clear = reinterpret_cast<int32_t*>(ws + L.err);
+    q.clear_words = static_cast<int>((L.clear_end - L.err) / 4);
+    MOE_CUDA(launch_quantize_rows(q, s));
     if (q8_ffn_supported(rows, E, I)) {
         Q8FfnArgs f;
         f.x_q = xq;
@@ -834,7 +851,14 @@ static moe_status w8a8_ffn(const void* x_perm, const int32_t* offsets, const int
     g.out = act;
     MOE_CUDA(launch_q8_gemm(g, s));
     if (mid) record_event(mid, s);
-    MOE_CUDA(launch_quantize_rows(act, rows, I, false, aq, as, s));
+    q = QuantizeArgs();
+    q.x = act;
+    q.rows = rows;
+    q.K = I;
+    q.bf16 = false;
+    q.q = aq;
+    q.scale = as;
+    MOE_CUDA(launch_quantize_rows(q, s));
     g = Q8GemmArgs();
     g.a_q = aq;
     g.a_scale = as;
@@ -873,7 +897,7 @@ moe_status moe_expert_ffn_w8a8(const void* x_perm, const int32_t* offsets, const
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     char* ws = static_cast<char*>(workspace);
     int32_t* err = reinterpret_cast<int32_t*>(ws + L.err);
-    return w8a8_ffn(x_perm, offsets, fc1_q, fc1_scale, fc2_q, fc2_scale, rows, H, E, I,
+    return w8a8_ffn(x_perm, nullptr, 0, 1, offsets, fc1_q, fc1_scale, fc2_q, fc2_scale, rows, H, E, I,
                     make_ffn_attrs(act, fc1_layout, fc1_bias, fc2_bias), y_perm, ws, L, err, s, nullptr);
 }
 
@@ -923,9 +947,9 @@ moe_status moe_forward_w8a8(const void* hidden, const void* norm_weight, float n
                        i32(L.perm_src), i32(L.perm_dst), i32(L.tile_counts), i32(0), nullptr, 0};
     moe_status st = staged_routing(path, hidden, router_w, router_bias, T, H, E, k, normalize, true, rb, s);
     if (st != MOE_OK) return st;
-    MOE_CUDA(gather_rows(hidden, rb.perm_src, rb.perm_dst, rb.offsets, T, E, k, H, MOE_BF16, ws + L.x_perm, s));
     record(2, s);
-    st = w8a8_ffn(ws + L.x_perm, rb.offsets, fc1_q, fc1_scale, fc2_q, fc2_scale, rows, H, E, I,
+    // the permutation of the rows goes with their rounding
+    st = w8a8_ffn(hidden, rb.perm_dst, T, k, rb.offsets, fc1_q, fc1_scale, fc2_q, fc2_scale, rows, H, E, I,
                   make_ffn_attrs(act, fc1_layout, fc1_bias, fc2_bias), ws + L.y, ws + L.ffn,
                   w8a8_layout(rows, H, E, I), i32(0), s, g_events_on ? g_events[3] : nullptr);
     if (st != MOE_OK) return st;

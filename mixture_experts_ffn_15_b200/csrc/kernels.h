@@ -186,10 +186,18 @@ cudaError_t launch_ffn_pair(const void* x_perm, const int32_t* offsets, const vo
                             int32_t* err, cudaStream_t s, cudaEvent_t mid, const FfnAttrs& ep);
 
 // ---------------------------------------------------------------- quantize.cu
-// q [rows, K] int8 and scale [rows] of x [rows, K] (bf16 or float32; K a multiple of 8); the
-// same launch zeroes `clear_words` 32-bit words at `clear`.
-cudaError_t launch_quantize_rows(const void* x, int rows, int K, bool bf16, int8_t* q, float* scale,
-                                 cudaStream_t s, int32_t* clear = nullptr, int clear_words = 0);
+struct QuantizeArgs {
+    const void* x = nullptr;             // [rows, K] bf16 or float32, K a multiple of 8
+    int rows = 0, K = 0;
+    bool bf16 = true;
+    int8_t* q = nullptr;                 // [rows, K]; with perm_dst [rows_out, K]
+    float* scale = nullptr;              // [rows] ([rows_out])
+    const int32_t* perm_dst = nullptr;   // [rows, k]: row t goes to rows perm_dst[t, :] of q
+    int k = 1, rows_out = 0;
+    int32_t* clear = nullptr;            // zeroed by the same launch
+    int clear_words = 0;
+};
+cudaError_t launch_quantize_rows(const QuantizeArgs& a, cudaStream_t s);
 
 // ---------------------------------------------------------------- gemm_q8.cu
 // One grouped product of int8 rows and int8 weights (K a multiple of 16, N of 32).

@@ -13,9 +13,14 @@
 // bf16 the first rounding is exact (quantize.cuh says why), which matters: x = amax / 2 is a
 // half, and one value in 600 of a normal row is.
 //
+// With perm_dst, row t's int8 row and scale go to every row perm_dst[t k + j] instead (the
+// permuted rows of the layer: the token rows are read and rounded once, not k times).
+//
 // One pass over the row: a row's threads keep their vectors of 8 elements in registers
 // between the maximum and the rounding (rows longer than kRegVec vectors a thread read the
 // rest again, from L2).  Bound by HBM: rows K (2 or 4) bytes read, rows (K + 4) written.
+#include <type_traits>
+
 #include "common.cuh"
 #include "kernels.h"
 #include "quantize.cuh"
@@ -64,10 +69,11 @@ struct Vec8 {
 };
 
 // TPR threads (a power of two, 32 .. 256) share a row, kRegVec vectors a thread in registers.
-template <bool BF16, int TPR, int kRegVec>
+template <bool BF16, int TPR, int kRegVec, bool SCATTER>
 __global__ void __launch_bounds__(kQThreads)
 quantize_rows_kernel(const void* __restrict__ x, int rows, int K, int8_t* __restrict__ q,
-                     float* __restrict__ scale, int32_t* __restrict__ clear, int clear_words) {
+                     float* __restrict__ scale, const int32_t* __restrict__ perm_dst, int k, int rows_out,
+                     int32_t* __restrict__ clear, int clear_words) {
     constexpr int kRows = kQThreads / TPR;   // rows of a block
     __shared__ uint32_t s_max[kQThreads / 32];
     pdl_wait();
@@ -102,8 +108,20 @@ quantize_rows_kernel(const void* __restrict__ x, int rows, int K, int8_t* __rest
     }
     if (!live) return;
     const RowQuant rq = row_quant(m);
-    if (t == 0) scale[row] = rq.scale;
-    uint2* out = reinterpret_cast<uint2*>(q) + row * nvec;
+    // copies of the row: k permuted ones, or itself
+    auto each = [&](auto fn) {
+        if constexpr (!SCATTER) {
+            fn(row);
+            return;
+        }
+#pragma unroll 4
+        for (int j = 0; j < k; ++j) {
+            const int to = __ldg(perm_dst + row * k + j);
+            if (static_cast<unsigned>(to) < static_cast<unsigned>(rows_out)) fn(static_cast<long long>(to));
+        }
+    };
+    if (t == 0) each([&](long long to) { scale[to] = rq.scale; });
+    uint2* out = reinterpret_cast<uint2*>(q);
     bool sure = ordinary(rq) && !(BF16 && bf16_exception(m));
     if (sure) {
         float far = 0.f, f[8];
@@ -113,7 +131,8 @@ quantize_rows_kernel(const void* __restrict__ x, int rows, int K, int8_t* __rest
 #pragma unroll
             for (int i = 0; i < 8; ++i) n[i] = quantize_fast<true>(f[i], 1.f, rq.inv, &far);
             if (BF16) far = 0.f;
-            out[v] = make_uint2(pack_s8x4(n), pack_s8x4(n + 4));
+            const uint2 o = make_uint2(pack_s8x4(n), pack_s8x4(n + 4));
+            each([&](long long to) { out[to * nvec + v] = o; });
         };
 #pragma unroll
         for (int j = 0; j < kRegVec; ++j)
@@ -135,19 +154,20 @@ quantize_rows_kernel(const void* __restrict__ x, int rows, int K, int8_t* __rest
             w.get(f);
 #pragma unroll
             for (int i = 0; i < 8; ++i) n[i] = quantize_exact(f[i], rq.pre, rq.inv, rq.amax);
-            out[v] = make_uint2(pack_s8x4(n), pack_s8x4(n + 4));
+            const uint2 o = make_uint2(pack_s8x4(n), pack_s8x4(n + 4));
+            each([&](long long to) { out[to * nvec + v] = o; });
         }
     }
 }
 
 template <bool BF16>
-cudaError_t launch(const void* x, int rows, int K, int8_t* q, float* scale, cudaStream_t s, int32_t* clear,
-                   int clear_words) {
+cudaError_t launch(const QuantizeArgs& a, cudaStream_t s) {
+    const int rows = a.rows, K = a.K;
     const int nvec = K / 8;
     auto go = [&](auto kern, int tpr) {
         const int per = kQThreads / tpr;
-        return launch_k(kern, dim3(static_cast<unsigned>((rows + per - 1) / per)), dim3(kQThreads), 0, s, x, rows, K, q,
-                        scale, clear, clear_words);
+        return launch_k(kern, dim3(static_cast<unsigned>((rows + per - 1) / per)), dim3(kQThreads), 0, s, a.x,
+                        rows, K, a.q, a.scale, a.perm_dst, a.k, a.rows_out, a.clear, a.clear_words);
     };
     // Many rows: as few threads a row as hold it in registers, for many loads in flight and
     // no barrier.  Few rows (less than four blocks an SM): spread a row, for latency.
@@ -157,21 +177,30 @@ cudaError_t launch(const void* x, int rows, int K, int8_t* q, float* scale, cuda
     while (tpr < kQThreads && (tpr * kReg < nvec || (tpr < nvec && static_cast<long long>(rows) * tpr < 4 * kQThreads * sms)))
         tpr *= 2;
     const bool few = tpr * kFew >= nvec;
-    switch (tpr) {
-        case 32: return few ? go(quantize_rows_kernel<BF16, 32, kFew>, 32) : go(quantize_rows_kernel<BF16, 32, kReg>, 32);
-        case 64: return few ? go(quantize_rows_kernel<BF16, 64, kFew>, 64) : go(quantize_rows_kernel<BF16, 64, kReg>, 64);
-        case 128: return few ? go(quantize_rows_kernel<BF16, 128, kFew>, 128) : go(quantize_rows_kernel<BF16, 128, kReg>, 128);
-        default: return few ? go(quantize_rows_kernel<BF16, 256, kFew>, 256) : go(quantize_rows_kernel<BF16, 256, kReg>, 256);
+    auto pick = [&](auto scatter) {
+        constexpr bool S = decltype(scatter)::value;
+        switch (tpr) {
+            case 32: return few ? go(quantize_rows_kernel<BF16, 32, kFew, S>, 32) : go(quantize_rows_kernel<BF16, 32, kReg, S>, 32);
+            case 64: return few ? go(quantize_rows_kernel<BF16, 64, kFew, S>, 64) : go(quantize_rows_kernel<BF16, 64, kReg, S>, 64);
+            case 128:
+                return few ? go(quantize_rows_kernel<BF16, 128, kFew, S>, 128) : go(quantize_rows_kernel<BF16, 128, kReg, S>, 128);
+            default:
+                return few ? go(quantize_rows_kernel<BF16, 256, kFew, S>, 256) : go(quantize_rows_kernel<BF16, 256, kReg, S>, 256);
+        }
+    };
+    if constexpr (BF16) {
+        if (a.perm_dst) return pick(std::true_type());
+    } else if (a.perm_dst) {
+        return cudaErrorInvalidValue;   // the layer's input is bf16
     }
+    return pick(std::false_type());
 }
 
 }  // namespace
 
-cudaError_t launch_quantize_rows(const void* x, int rows, int K, bool bf16, int8_t* q, float* scale,
-                                 cudaStream_t s, int32_t* clear, int clear_words) {
-    if (rows <= 0) return cudaSuccess;
-    return bf16 ? launch<true>(x, rows, K, q, scale, s, clear, clear_words)
-                : launch<false>(x, rows, K, q, scale, s, clear, clear_words);
+cudaError_t launch_quantize_rows(const QuantizeArgs& a, cudaStream_t s) {
+    if (a.rows <= 0) return cudaSuccess;
+    return a.bf16 ? launch<true>(a, s) : launch<false>(a, s);
 }
 
 }  // namespace moe

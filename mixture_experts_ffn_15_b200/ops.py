@@ -223,13 +223,14 @@ def quantize_rows(x, q=None, scale=None, stream=None):
     with here:
         if q is None:
             q = torch.empty_like(x, dtype=torch.int8)
+        else:
+            _same_device(x, _need(q, "q", torch.int8, (rows, K)))
         if scale is None:
-            scale = x.new_empty((rows,), dtype=torch.float32)
-        _need(q, "q", torch.int8, (rows, K))
-        _need(scale, "scale", torch.float32, (rows,))
-        _same_device(x, q, scale)
-        check(_lib().moe_quantize_rows(_addr(x), rows, K, _dtcode(x), _addr(q), _addr(scale),
-                                       s), "moe_quantize_rows")
+            scale = x.new_empty(rows, dtype=torch.float32)
+        else:
+            _same_device(x, _need(scale, "scale", torch.float32, (rows,)))
+        check(_lib().moe_quantize_rows(x.data_ptr(), rows, K, _dtcode(x), q.data_ptr(),
+                                       scale.data_ptr(), s), "moe_quantize_rows")
     return q, scale
 
 

@@ -1,9 +1,10 @@
 """The balance loss, its counts and its gradient on the GPU against float64.
 
-Bounds: a float32 softmax probability is within 24 U32 + 2 |logit - max| U32 of its exact
-value (the difference rounds once, the exponential is within 2 ulp, the sum of E terms by a
-tree of depth 5 on up to 8 terms a lane rounds 13 times, the quotient and the product once
-each), with U32 = 2^-24; logits here stay within 20 of their row's maximum: 64 U32 relative.
+Bounds, with U32 = 2^-24: the difference logit - max rounds once, its product with log2 e once,
+log2 e itself is off by less than 0.3 U32: 2.3 |logit - max| U32 in the exponent; the
+exponential is within 2 ulp (4 U32), the sum of E terms by a tree of depth 5 on up to 8 terms
+a lane rounds 12 times, the quotient and the product once each: (18 + 2.3 |logit - max|) U32.
+Logits here stay within 20 of their row's maximum: 64 U32 relative.
 P adds float32 sums of at most 27 such terms a lane, over 5 shuffles and 32 warps: another
 64 U32 (the blocks' sums are added in float64).
 The loss is a sum of non-negative terms f P: the same relative bound, and its own rounding.
