@@ -497,49 +497,58 @@ q8_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
         }
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA issuer
-        if (lead && lane == 0) {
+        // The whole warp walks the units in step, one elected lane issues.
+        if (lead) {
             int stage = 0, acc = 0;
             uint32_t phase = 0, acc_phase = 0;
             auto rows_of_next = [&]() {   // the next unit's rows, 0 if the wait gave up
                 int n = 0;
                 if (mbar_wait(smem_u32(&ufull[plan.slot]), plan.phase, abort_flag, kWaitNs)) n = s_unit[plan.slot].nrows;
-                mbar_arrive(smem_u32(&uempty[plan.slot]));
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&uempty[plan.slot]));
                 plan.next();
                 return n;
             };
+            const uint64_t a_desc = smem_desc_sw128(smem_u32(sA)), b_desc = smem_desc_sw128(smem_u32(sB));
+            const uint32_t a_lo = static_cast<uint32_t>(a_desc), b_lo = static_cast<uint32_t>(b_desc);
+            const uint32_t hi = static_cast<uint32_t>(a_desc >> 32);
+            const int steps = (p.K + 31) / 32;            // MMAs of a unit: none past K
+            constexpr int kStep = kPSub * (kBK / 32);     // of a whole stage
             int nrows = pair < units ? rows_of_next() : 0, nrows_next = 0;
             for (long long u = pair; u < units && !*abort_flag; u += npairs) {
                 const uint32_t idesc = idesc_s8_s32(2 * kPWRows, unit_n(nrows));
-                if (!mbar_wait(smem_u32(&tempty[acc]), acc_phase ^ 1u, abort_flag, kWaitNs)) break;
+                if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&tempty[acc]), acc_phase ^ 1u, abort_flag, kWaitNs))) break;
                 tc_fence_after();
                 const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * kPAccCols);
                 bool ok = true;
-                for (int kb0 = 0; kb0 < nk; kb0 += kPSub) {
-                    const int ns = min(kPSub, nk - kb0);
-                    if (!mbar_wait(smem_u32(&full[stage]), phase, abort_flag, kWaitNs)) {
+                for (int s0 = 0; s0 < steps; s0 += kStep) {
+                    if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&full[stage]), phase, abort_flag, kWaitNs))) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    for (int j = 0; j < ns; ++j) {
-                        const int sl = stage * kPSub + j;
-                        const uint32_t a0 = smem_u32(sA + sl * kPABytes), b0 = smem_u32(sB + sl * kPBBytes);
+                    const uint32_t la = a_lo + static_cast<uint32_t>(stage * (kPSub * kPABytes >> 4));
+                    const uint32_t lb = b_lo + static_cast<uint32_t>(stage * (kPSub * kPBBytes >> 4));
+                    if (elect_one()) {
 #pragma unroll
-                        for (int kk = 0; kk < kBK / 32; ++kk)
-                            if ((kb0 + j) * kBK + kk * 32 < p.K)   // nothing but zeros past K
-                                umma_s8_pair(d_tmem, smem_desc_sw128(a0 + kk * 32), smem_desc_sw128(b0 + kk * 32), idesc,
-                                             (kb0 + j > 0 || kk > 0) ? 1u : 0u);
+                        for (int i = 0; i < kStep; ++i)
+                            if (s0 + i < steps)
+                                umma_s8_pair_lo(d_tmem, la + (i / 4) * (kPABytes >> 4) + (i % 4) * 2,
+                                                lb + (i / 4) * (kPBBytes >> 4) + (i % 4) * 2, hi, idesc,
+                                                i > 0 ? 1u : (s0 > 0 ? 1u : 0u));
+                        umma_commit_pair(smem_u32(&empty[stage]), 0x3);
                     }
-                    umma_commit_pair(smem_u32(&empty[stage]), 0x3);
+                    __syncwarp();
                     if (++stage == kPStages) {
                         stage = 0;
                         phase ^= 1u;
                     }
                     // read behind the first MMAs, used after the last
-                    if (kb0 == 0 && u + npairs < units) nrows_next = rows_of_next();
+                    if (s0 == 0 && u + npairs < units) nrows_next = rows_of_next();
                 }
                 if (!ok) break;
-                umma_commit_pair(smem_u32(&tfull[acc]), 0x3);
+                if (elect_one()) umma_commit_pair(smem_u32(&tfull[acc]), 0x3);
+                __syncwarp();
                 acc ^= 1;
                 if (acc == 0) acc_phase ^= 1u;
                 nrows = nrows_next;
