@@ -129,9 +129,11 @@ bool valid_w8a8_ffn(int H, int I) {
 
 // Workspace of the int8 expert FFN: error word and, for few rows per expert, the counters of
 // its one launch (both cleared by the row quantiser), the int8 rows and scales of x_perm,
-// the float32 activations, their int8 rows and scales.
+// the float32 activations, their int8 rows and scales.  The int8 rows start on 128-byte boundaries: a 128-byte slice of a row then lies in one line of
+// the L2 cache, which the loads of the products go by (rows of 704 bytes: two lines each).
 struct W8a8Layout {
     size_t err, counters, clear_end, xq, xs, act, aq, as, total;
+    int ldx, lda;   // bytes a row of xq, aq
 };
 
 W8a8Layout w8a8_layout(int rows, int H, int E, int I) {
@@ -141,10 +143,12 @@ W8a8Layout w8a8_layout(int rows, int H, int E, int I) {
     L.err = c.take(kAlign);
     L.counters = c.take(q8_ffn_supported(rows, E, I) ? static_cast<size_t>(q8_ffn_counters(rows, E)) * 4 : 0);
     L.clear_end = c.off;
-    L.xq = c.take(r * H);
+    L.ldx = (H + 127) / 128 * 128;
+    L.lda = (I + 127) / 128 * 128;
+    L.xq = c.take(r * L.ldx);
     L.xs = c.take(r * 4);
     L.act = c.take(r * I * 4);
-    L.aq = c.take(r * I);
+    L.aq = c.take(r * L.lda);
     L.as = c.take(r * 4);
     L.total = c.off;
     return L;
@@ -802,6 +806,7 @@ static moe_status w8a8_ffn(const void* x, const int32_t* perm_dst, int T, int k,
     q.rows = perm_dst ? T : rows;
     q.K = H;
     q.q = xq;
+    q.ldq = L.ldx;
     q.scale = xs;
     q.perm_dst = perm_dst;
     q.k = k;
@@ -812,6 +817,8 @@ static moe_status w8a8_ffn(const void* x, const int32_t* perm_dst, int T, int k,
     if (q8_ffn_supported(rows, E, I)) {
         Q8FfnArgs f;
         f.x_q = xq;
+        f.ldx = L.ldx;
+        f.lda = L.lda;
         f.x_scale = xs;
         f.offsets = offsets;
         f.fc1_q = fc1_q;
@@ -835,6 +842,7 @@ static moe_status w8a8_ffn(const void* x, const int32_t* perm_dst, int T, int k,
     }
     Q8GemmArgs g;
     g.a_q = xq;
+    g.lda = L.ldx;
     g.a_scale = xs;
     g.w_q = fc1_q;
     g.w_scale = fc1_scale;
@@ -857,10 +865,12 @@ static moe_status w8a8_ffn(const void* x, const int32_t* perm_dst, int T, int k,
     q.K = I;
     q.bf16 = false;
     q.q = aq;
+    q.ldq = L.lda;
     q.scale = as;
     MOE_CUDA(launch_quantize_rows(q, s));
     g = Q8GemmArgs();
     g.a_q = aq;
+    g.lda = L.lda;
     g.a_scale = as;
     g.w_q = fc2_q;
     g.w_scale = fc2_scale;

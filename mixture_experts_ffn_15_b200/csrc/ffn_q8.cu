@@ -71,7 +71,8 @@ struct Params {
     const __nv_bfloat16* b1;  // [E, 2I] or nullptr
     const __nv_bfloat16* b2;  // [E, H] or nullptr
     float* act;               // [rows, I] scratch
-    int8_t* aq;               // [rows, I] scratch
+    int8_t* aq;               // [rows, I] scratch, rows lda bytes apart
+    int lda;
     float* as;                // [rows] scratch
     __nv_bfloat16* y;         // [rows, H]
     int32_t* done;            // [chunks] finished fc1 epilogue warps, zero on entry
@@ -114,10 +115,10 @@ __device__ __forceinline__ void fence_proxy_async_global() { asm volatile("fence
 
 // The int8 rows of activation rows row and row + 1 (if `two`), by one warp.
 __device__ __forceinline__ void round_rows(const Params& p, int row, bool two, int lane) {
-    const int nvec = p.I / 4;
+    const int nvec = p.I / 4, ldw = p.lda / 4;
     const float4* x0 = reinterpret_cast<const float4*>(p.act + static_cast<size_t>(row) * p.I);
     const float4* x1 = two ? x0 + nvec : x0;
-    uint32_t* out = reinterpret_cast<uint32_t*>(p.aq + static_cast<size_t>(row) * p.I);
+    uint32_t* out = reinterpret_cast<uint32_t*>(p.aq + static_cast<size_t>(row) * p.lda);
     auto top = [](const float4& v) {
         return max(max(__float_as_uint(v.x) & 0x7fffffffu, __float_as_uint(v.y) & 0x7fffffffu),
                    max(__float_as_uint(v.z) & 0x7fffffffu, __float_as_uint(v.w) & 0x7fffffffu));
@@ -156,12 +157,12 @@ __device__ __forceinline__ void round_rows(const Params& p, int row, bool two, i
     for (int j = 0; j < kHold; ++j)
         if (lane + 32 * j < nvec) {
             out[lane + 32 * j] = fast(h0[j], q0);
-            if (two) out[nvec + lane + 32 * j] = fast(h1[j], q1);
+            if (two) out[ldw + lane + 32 * j] = fast(h1[j], q1);
         }
 #pragma unroll 4
     for (int v = lane + 32 * kHold; v < nvec; v += 32) {
         out[v] = fast(__ldcg(x0 + v), q0);
-        if (two) out[nvec + v] = fast(__ldcg(x1 + v), q1);
+        if (two) out[ldw + v] = fast(__ldcg(x1 + v), q1);
     }
     if (!ordinary(q0) || !ordinary(q1) || !(far <= kSureDistance)) {   // this lane's values again, exactly
         auto exact = [](const float4& v, const RowQuant& q) {
@@ -172,7 +173,7 @@ __device__ __forceinline__ void round_rows(const Params& p, int row, bool two, i
 #pragma unroll 1
         for (int v = lane; v < nvec; v += 32) {
             out[v] = exact(__ldcg(x0 + v), q0);
-            if (two) out[nvec + v] = exact(__ldcg(x1 + v), q1);
+            if (two) out[ldw + v] = exact(__ldcg(x1 + v), q1);
         }
     }
     if (lane == 0) {
@@ -553,12 +554,12 @@ cudaError_t launch_q8_ffn(const Q8FfnArgs& a, cudaStream_t s) {
     CUtensorMap w1, x, w2, act;
     if (!tmap::pairs8(&w1, a.fc1_q, a.E, 2 * a.I, a.H, kWRows / 2, a.ep.fc1_chunked)) return cudaErrorInvalidValue;
     if (!tmap::pairs8(&w2, a.fc2_q, a.E, a.H, a.I, kWRows / 2, false)) return cudaErrorInvalidValue;
-    if (!tmap::matrix8(&x, a.x_q, a.rows, a.H, kBox)) return cudaErrorInvalidValue;
-    if (!tmap::matrix8(&act, a.act_q, a.rows, a.I, kBox)) return cudaErrorInvalidValue;
+    if (!tmap::matrix8(&x, a.x_q, a.rows, a.H, kBox, a.ldx)) return cudaErrorInvalidValue;
+    if (!tmap::matrix8(&act, a.act_q, a.rows, a.I, kBox, a.lda)) return cudaErrorInvalidValue;
     const int chunks = a.rows / kTok + a.E + 1;
     const Params p{a.offsets, a.E, a.rows, a.H, a.I, a.x_scale, a.ep.fc1_scale, a.ep.fc2_scale,
                    static_cast<const __nv_bfloat16*>(a.ep.fc1_bias), static_cast<const __nv_bfloat16*>(a.ep.fc2_bias),
-                   a.act, a.act_q, a.act_scale, static_cast<__nv_bfloat16*>(a.y), a.counters, a.counters + chunks,
+                   a.act, a.act_q, a.lda, a.act_scale, static_cast<__nv_bfloat16*>(a.y), a.counters, a.counters + chunks,
                    a.counters + 2 * chunks, a.err, a.ep.act, a.ep.fc1_chunked};
     static bool done[64] = {false};
     int dev = 0;

@@ -816,7 +816,7 @@ template <int MODE>
 cudaError_t stream_product(const Q8GemmArgs& a, const Q8Params& p, cudaStream_t s) {
     CUtensorMap w, x;
     if (!tmap::pairs8(&w, a.w_q, a.E, a.N, a.K, kSWRows / 2, false)) return cudaErrorInvalidValue;
-    if (!tmap::matrix8(&x, a.a_q, a.rows, a.K, kSBox)) return cudaErrorInvalidValue;
+    if (!tmap::matrix8(&x, a.a_q, a.rows, a.K, kSBox, a.lda ? a.lda : a.K)) return cudaErrorInvalidValue;
     const long long units = stream_units(a);
     const int sms = device_sm_count(), nk = (a.K + kBK - 1) / kBK;
     int cs = 8;
@@ -831,7 +831,7 @@ cudaError_t product(const Q8GemmArgs& a, const Q8Params& p, cudaStream_t s) {
     const bool chunked = a.swiglu && a.fc1_chunked;
     if (MODE == OUT_SWIGLU || !use_stream(a)) {
         if (!tmap::quads8(&w, a.w_q, a.E, a.N, a.K, chunked)) return cudaErrorInvalidValue;
-        if (!tmap::matrix8(&x, a.a_q, a.rows, a.K, kPBox)) return cudaErrorInvalidValue;
+        if (!tmap::matrix8(&x, a.a_q, a.rows, a.K, kPBox, a.lda ? a.lda : a.K)) return cudaErrorInvalidValue;
         const long long units = (static_cast<long long>((a.rows + kPTok - 1) / kPTok) + a.E) *
                                 ((a.N + 2 * kPWRows - 1) / (2 * kPWRows));
         return launch_pair<MODE>(w, x, p, units, s);

@@ -191,6 +191,7 @@ struct QuantizeArgs {
     int rows = 0, K = 0;
     bool bf16 = true;
     int8_t* q = nullptr;                 // [rows, K]; with perm_dst [rows_out, K]
+    int ldq = 0;                         // bytes from row to row of q, a multiple of 8 (0: K)
     float* scale = nullptr;              // [rows] ([rows_out])
     const int32_t* perm_dst = nullptr;   // [rows, k]: row t goes to rows perm_dst[t, :] of q
     int k = 1, rows_out = 0;
@@ -203,6 +204,7 @@ cudaError_t launch_quantize_rows(const QuantizeArgs& a, cudaStream_t s);
 // One grouped product of int8 rows and int8 weights (K a multiple of 16, N of 32).
 struct Q8GemmArgs {
     const int8_t* a_q = nullptr;       // [rows, K]
+    int lda = 0;                       // bytes from row to row of a_q, a multiple of 16 (0: K)
     const float* a_scale = nullptr;    // [rows]
     const int8_t* w_q = nullptr;       // [E, N, K]
     const float* w_scale = nullptr;    // [E, N]
@@ -225,15 +227,16 @@ cudaError_t launch_q8_gemm(const Q8GemmArgs& a, cudaStream_t s);
 bool q8_ffn_supported(int rows, int E, int I);
 int q8_ffn_counters(int rows, int E);   // int32 words it needs, zero on entry
 struct Q8FfnArgs {
-    const int8_t* x_q = nullptr;       // [rows, H]
+    const int8_t* x_q = nullptr;       // [rows, H], rows ldx bytes apart
     const float* x_scale = nullptr;    // [rows]
     const int32_t* offsets = nullptr;  // [E + 1]
     const int8_t* fc1_q = nullptr;     // [E, 2I, H]
     const int8_t* fc2_q = nullptr;     // [E, H, I]
     int rows = 0, H = 0, E = 0, I = 0;
+    int ldx = 0, lda = 0;              // row strides of x_q and act_q, multiples of 16
     FfnAttrs ep;                       // attributes, layout, biases, weight scales
     float* act = nullptr;              // [rows, I] scratch
-    int8_t* act_q = nullptr;           // [rows, I] scratch
+    int8_t* act_q = nullptr;           // [rows, I] scratch, rows lda bytes apart
     float* act_scale = nullptr;        // [rows] scratch
     int32_t* counters = nullptr;
     int32_t* err = nullptr;

@@ -71,7 +71,7 @@ struct Vec8 {
 // TPR threads (a power of two, 32 .. 256) share a row, kRegVec vectors a thread in registers.
 template <bool BF16, int TPR, int kRegVec, bool SCATTER>
 __global__ void __launch_bounds__(kQThreads)
-quantize_rows_kernel(const void* __restrict__ x, int rows, int K, int8_t* __restrict__ q,
+quantize_rows_kernel(const void* __restrict__ x, int rows, int K, int8_t* __restrict__ q, int ldq,
                      float* __restrict__ scale, const int32_t* __restrict__ perm_dst, int k, int rows_out,
                      int32_t* __restrict__ clear, int clear_words) {
     constexpr int kRows = kQThreads / TPR;   // rows of a block
@@ -122,6 +122,7 @@ quantize_rows_kernel(const void* __restrict__ x, int rows, int K, int8_t* __rest
     };
     if (t == 0) each([&](long long to) { scale[to] = rq.scale; });
     uint2* out = reinterpret_cast<uint2*>(q);
+    const int ldv = ldq / 8;
     bool sure = ordinary(rq) && !(BF16 && bf16_exception(m));
     if (sure) {
         float far = 0.f, f[8];
@@ -132,7 +133,7 @@ quantize_rows_kernel(const void* __restrict__ x, int rows, int K, int8_t* __rest
             for (int i = 0; i < 8; ++i) n[i] = quantize_fast<true>(f[i], 1.f, rq.inv, &far);
             if (BF16) far = 0.f;
             const uint2 o = make_uint2(pack_s8x4(n), pack_s8x4(n + 4));
-            each([&](long long to) { out[to * nvec + v] = o; });
+            each([&](long long to) { out[to * ldv + v] = o; });
         };
 #pragma unroll
         for (int j = 0; j < kRegVec; ++j)
@@ -155,7 +156,7 @@ quantize_rows_kernel(const void* __restrict__ x, int rows, int K, int8_t* __rest
 #pragma unroll
             for (int i = 0; i < 8; ++i) n[i] = quantize_exact(f[i], rq.pre, rq.inv, rq.amax);
             const uint2 o = make_uint2(pack_s8x4(n), pack_s8x4(n + 4));
-            each([&](long long to) { out[to * nvec + v] = o; });
+            each([&](long long to) { out[to * ldv + v] = o; });
         }
     }
 }
@@ -167,7 +168,7 @@ cudaError_t launch(const QuantizeArgs& a, cudaStream_t s) {
     auto go = [&](auto kern, int tpr) {
         const int per = kQThreads / tpr;
         return launch_k(kern, dim3(static_cast<unsigned>((rows + per - 1) / per)), dim3(kQThreads), 0, s, a.x,
-                        rows, K, a.q, a.scale, a.perm_dst, a.k, a.rows_out, a.clear, a.clear_words);
+                        rows, K, a.q, a.ldq ? a.ldq : K, a.scale, a.perm_dst, a.k, a.rows_out, a.clear, a.clear_words);
     };
     // Many rows: as few threads a row as hold it in registers, for many loads in flight and
     // no barrier.  Few rows (less than four blocks an SM): spread a row, for latency.

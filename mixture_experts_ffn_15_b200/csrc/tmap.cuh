@@ -216,9 +216,11 @@ inline void narrow(View* v, int K) {
     v->box[0] = static_cast<cuuint32_t>(kBoxK8);
 }
 
-inline bool matrix8_view(View* v, long long rows, int K, int box_rows) {
-    if (!matrix_view(v, rows, K, box_rows)) return false;
+// Rows of `ld` bytes (a multiple of 16), K of them used.
+inline bool matrix8_view(View* v, long long rows, int K, int box_rows, int ld) {
+    if (ld < K || ld % 16 != 0 || !matrix_view(v, rows, K, box_rows)) return false;
     narrow(v, K);
+    v->strides[0] = static_cast<cuuint64_t>(ld);
     return true;
 }
 
@@ -239,9 +241,9 @@ inline bool quads8_view(View* v, int E, int n, int K, bool fc1_chunked) {
     return true;
 }
 
-inline bool matrix8(CUtensorMap* m, const void* p, long long rows, int K, int box_rows) {
+inline bool matrix8(CUtensorMap* m, const void* p, long long rows, int K, int box_rows, int ld) {
     View v;
-    return matrix8_view(&v, rows, K, box_rows) && encode(m, v, p);
+    return matrix8_view(&v, rows, K, box_rows, ld) && encode(m, v, p);
 }
 
 inline bool pairs8(CUtensorMap* m, const void* w, int E, int n, int K, int box_pairs, bool fc1_chunked) {

@@ -23,7 +23,7 @@ int main(int argc, char** argv) {
     if (argc != 4) return 2;
     const int E = std::atoi(argv[1]), n = std::atoi(argv[2]), K = std::atoi(argv[3]);
     View v;
-    print("rows", moe::tmap::matrix8_view(&v, E * 7, K, 16), v);
+    print("rows", moe::tmap::matrix8_view(&v, E * 7, K, 16, K), v);
     for (int c = 0; c < 2; ++c) {
         print(c ? "pairs_chunked" : "pairs", moe::tmap::pairs8_view(&v, E, n, K, 64, c != 0), v);
         print(c ? "quads_chunked" : "quads", moe::tmap::quads8_view(&v, E, n, K, c != 0), v);
