@@ -434,10 +434,10 @@ def quantize_rows(x):
 
 
 def matmul_q8(a_q, a_scale, w_q, w_scale, bias=None):
-    """(sum_k a_q[r, k] w_q[n, k]) a_scale[r] w_scale[n] + bias[n]: whole-number sums, the
-    rest float64."""
-    s = np.asarray(a_q, dtype=np.int64) @ np.asarray(w_q, dtype=np.int64).T
-    y = s.astype(np.float64) * np.asarray(a_scale, dtype=np.float64)[:, None] * \
+    """(sum_k a_q[r, k] w_q[n, k]) a_scale[r] w_scale[n] + bias[n] in float64, where the
+    whole-number sums are exact (far below 2^53)."""
+    s = np.asarray(a_q, dtype=np.float64) @ np.asarray(w_q, dtype=np.float64).T
+    y = s * np.asarray(a_scale, dtype=np.float64)[:, None] * \
         np.asarray(w_scale, dtype=np.float64)[None, :]
     return y if bias is None else y + np.asarray(bias, dtype=np.float64)[None, :]
 

@@ -80,6 +80,7 @@ PRODUCTS = [  # rows, K, N, E (0: dense), used experts
     (64, 704, 256, 0, None), (65, 272, 288, 0, None), (129, 400, 544, 0, None), (300, 1040, 512, 0, None),
     (777, 256, 1312, 0, None), (1, 64, 64, 3, None), (32, 256, 192, 16, None), (40, 2816, 96, 5, 2),
     (257, 192, 320, 4, None), (700, 320, 256, 7, 3), (2000, 128, 416, 256, None), (900, 528, 224, 2, 1),
+    (3000, 1152, 1056, 0, None), (2100, 832, 1504, 9, 6),   # CTA pairs, K of more than six blocks
 ]
 
 
@@ -109,6 +110,25 @@ def _product_ref(xv, off, w, ws, bv, dt, rows, N):
 @pytest.mark.parametrize("rows,K,N,E,used", PRODUCTS)
 def test_matmul_q8(rows, K, N, E, used, dt, bias):
     x, xv, off, w, ws, b, bv = _product_case(rows, K, N, E, used, dt, bias, rows + K + N)
+    q, s = moe.quantize_rows(x.cuda())
+    b = None if b is None else b.cuda()
+    if E:
+        out = moe.matmul_q8(q, s, dev(w), dev(ws), offsets=dev(off), bias=b, out_dtype=TORCH[dt])
+    else:
+        out = moe.matmul_q8(q, s, dev(w[0]), dev(ws[0]), bias=None if b is None else b[0], out_dtype=TORCH[dt])
+    y, bound = _product_ref(xv, off, w, ws, bv, dt, rows, N)
+    check(from_dev(out), y, bound, f"product {rows}x{K}x{N} E={E}")
+
+
+@pytest.mark.parametrize("rows,K,N,E,used,dt,bias", [
+    (20000, 16, 3104, 0, None, "bf16", True), (9001, 704, 6240, 0, None, "bf16", False),
+    (30000, 272, 1824, 3, 2, "f32", True), (12000, 768, 5152, 5, None, "bf16", True),
+    (24000, 80, 4768, 4, 3, "f32", False), (24001, 400, 4800, 60, 50, "bf16", True),
+])
+def test_matmul_q8_weights_kept_for_several_token_tiles(rows, K, N, E, used, dt, bias):
+    """Sizes at which a CTA pair keeps a weight tile for 2 to 4 token tiles (K of one to six
+    128-wide blocks, ragged tiles and groups, experts without rows)."""
+    x, xv, off, w, ws, b, bv = _product_case(rows, K, N, E, used, dt, bias, rows + K)
     q, s = moe.quantize_rows(x.cuda())
     b = None if b is None else b.cuda()
     if E:
@@ -179,6 +199,8 @@ FFNS = [  # rows, H, I, E, used, layout, act, biases
     (500, 256, 224, 2, 1, "chunked", STD, False),
     (1100, 512, 256, 3, None, "interleaved", STD, True),
     (900, 384, 704, 200, None, "chunked", OSS, False),
+    # many rows of short K: fc1's, or fc2's, weight tiles kept for several token tiles
+    (30000, 64, 1024, 3, 2, "chunked", OSS, True), (30000, 1824, 64, 2, None, "interleaved", STD, False),
 ]
 
 
