@@ -499,12 +499,15 @@ q8_ffn_kernel(const __grid_constant__ CUtensorMap tmW1, const __grid_constant__ 
                 }
             }
             tc_fence_before();
-            if (f1) __threadfence();
             __syncwarp();
             if (lane == 0) {
                 mbar_arrive(smem_u32(&tempty[acc]));
                 mbar_arrive(smem_u32(&uempty[at]));
-                if (f1) atomicAdd(p.done + d.chunk, 1);
+            }
+            if (f1) {
+                __threadfence();
+                __syncwarp();
+                if (lane == 0) atomicAdd(p.done + d.chunk, 1);
             }
             acc ^= 1;
             if (acc == 0) acc_phase ^= 1u;

@@ -647,12 +647,28 @@ q8_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
                     bias = *reinterpret_cast<const float4*>(sc.bias + quad * 32 + 4 * fj);
                     if (u + npairs < units) ok = read_unit(&d_next);
                 }
-                if (c >= d.nrows) break;
                 float2 sa2[4];
+                if (c < d.nrows) {
 #pragma unroll
-                for (int m = 0; m < 4; ++m) sa2[m] = *reinterpret_cast<const float2*>(sc.sa + c + 8 * m + 2 * ft);
-                tmem_wait_ld();
-                if (!wvalid) continue;
+                    for (int m = 0; m < 4; ++m) sa2[m] = *reinterpret_cast<const float2*>(sc.sa + c + 8 * m + 2 * ft);
+                    tmem_wait_ld();
+                }
+                if (c + 32 * kParts >= d.nrows || ci == kChunks - 1) {
+                    // this warp's last values are in registers: the accumulator and the scales
+                    // are free before the stores go out, which a release arrival behind them
+                    // would wait for (2800 cycles a unit; the bound at K = 704)
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(&tempty[acc]), 0));
+                        mbar_arrive(smem_u32(&sempty[acc]));
+                    }
+                    if (c >= d.nrows) break;
+                }
+                if (!wvalid) {
+                    if (c + 32 * kParts >= d.nrows) break;
+                    continue;
+                }
 #pragma unroll
                 for (int m = 0; m < 4; ++m) {
 #pragma unroll
@@ -677,12 +693,7 @@ q8_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
                         }
                     }
                 }
-            }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-                mbar_arrive_cluster(mapa_shared(smem_u32(&tempty[acc]), 0));
-                mbar_arrive(smem_u32(&sempty[acc]));
+                if (c + 32 * kParts >= d.nrows) break;
             }
             acc ^= 1;
             if (acc == 0) acc_phase ^= 1u;
