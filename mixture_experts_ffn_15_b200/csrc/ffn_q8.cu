@@ -27,6 +27,8 @@
 //        of 148 at 2048), and by the warp that completes a chunk it took 576 us at 2048 rows.
 // The launch is cooperative (every CTA resident), so a unit waited for is some running CTA's.
 // Every wait is bounded (2 s) and reports MOE_DEVERR_TIMEOUT.
+// Measured with the row quantiser in front: E = 128, H = 2816, I = 704, 32 rows (170 MB of the
+// used experts' weights) 43 us, 2048 rows (786 MB) 137 us, 5.7 TB/s.
 #include <cuda.h>
 
 #include "common.cuh"
@@ -400,7 +402,7 @@ q8_ffn_kernel(const __grid_constant__ CUtensorMap tmW1, const __grid_constant__ 
         pdl_wait();
         for (;;) {
             const int at = slot;
-            if (!mbar_wait(smem_u32(&ufull[at]), uphase, abort_flag, kWaitNs)) break;
+            if (!mbar_wait_warp(smem_u32(&ufull[at]), uphase, abort_flag, kWaitNs)) break;
             const Unit d = s_unit[at];
             if (d.kind == kNone) break;
             const bool f1 = d.kind == kFc1;
@@ -445,7 +447,7 @@ q8_ffn_kernel(const __grid_constant__ CUtensorMap tmW1, const __grid_constant__ 
         constexpr int kPairs = kTok / 2;
         // neighbouring pairs on different CTAs: a chunk's rows are rounded at once
         const int w0 = (warp - 8) * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x);
-        for (int v = w0; v < chunks * kPairs && !*abort_flag; v += kRoundWarps * static_cast<int>(gridDim.x)) {
+        for (int v = w0; v < chunks * kPairs; v += kRoundWarps * static_cast<int>(gridDim.x)) {
             const int chunk = v / kPairs, r0 = 2 * (v - chunk * kPairs);
             const int g = tile_group(chunk, p.E, s_pre);
             const int row0 = s_off[g] + (chunk - s_pre[g]) * kTok;
@@ -468,16 +470,16 @@ q8_ffn_kernel(const __grid_constant__ CUtensorMap tmW1, const __grid_constant__ 
         uint32_t acc_phase = 0;
         for (;;) {
             const int at = slot;
-            if (!mbar_wait(smem_u32(&ufull[at]), uphase, abort_flag, kWaitNs)) break;
+            if (!mbar_wait_warp(smem_u32(&ufull[at]), uphase, abort_flag, kWaitNs)) break;
             const Unit d = s_unit[at];
             if (d.kind == kNone) break;
             const bool f1 = d.kind == kFc1;
             const int wr = d.mt * kWRows + r;
             const bool wvalid = wr < (f1 ? 2 * p.I : p.H);   // even: a (gate, up) pair is valid or not as one
-            if (!mbar_wait(smem_u32(&sfull[at]), uphase, abort_flag, kWaitNs)) break;
+            if (!mbar_wait_warp(smem_u32(&sfull[at]), uphase, abort_flag, kWaitNs)) break;
             const Scales& sc = s_scales[at];
             const float sw = sc.sw[r], bias = sc.bias[r];
-            if (!mbar_wait(smem_u32(&tfull[acc]), acc_phase, abort_flag, kWaitNs)) break;
+            if (!mbar_wait_warp(smem_u32(&tfull[acc]), acc_phase, abort_flag, kWaitNs)) break;
             tc_fence_after();
             const uint32_t tb = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + static_cast<uint32_t>(acc * kTok);
 #pragma unroll 1

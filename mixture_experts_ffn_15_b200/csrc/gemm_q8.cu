@@ -12,7 +12,7 @@
 //   q8_stream_kernel  128 weight rows x up to 64 tokens per CTA: few rows per expert, each
 //                     weight byte read once, bound by HBM
 //   q8_pair_kernel    256 weight rows x up to 256 tokens per pair of CTAs: many rows per
-//                     expert, bound by the tensor cores
+//                     expert, bound by what an SM takes in from L2
 #include <cuda.h>
 
 #include "common.cuh"
@@ -55,19 +55,13 @@ __device__ __forceinline__ void channel(const Q8Params& p, int g, int wr, float*
                                 : bf16_at(static_cast<const __nv_bfloat16*>(p.bias), i);
 }
 
-// Output of one weight row (a lane; SwiGLU: gate rows on even lanes, up rows on odd ones)
-// and one token; called by whole warps.
+// Output of one weight row and one token.
 template <int MODE>
 __device__ __forceinline__ void store_one(const Q8Params& p, int row, int wr, float y, bool valid) {
-    if constexpr (MODE == OUT_SWIGLU) {
-        const float up = __shfl_xor_sync(0xffffffffu, y, 1);
-        if (valid && !(wr & 1))
-            static_cast<float*>(p.out)[static_cast<size_t>(row) * (p.N / 2) + (wr >> 1)] = swiglu_attr_fast(y, up, p.act);
-    } else if (valid) {
-        const size_t o = static_cast<size_t>(row) * p.N + wr;
-        if constexpr (MODE == OUT_BF16) static_cast<__nv_bfloat16*>(p.out)[o] = __float2bfloat16_rn(y);
-        else static_cast<float*>(p.out)[o] = y;
-    }
+    if (!valid) return;
+    const size_t o = static_cast<size_t>(row) * p.N + wr;
+    if constexpr (MODE == OUT_BF16) static_cast<__nv_bfloat16*>(p.out)[o] = __float2bfloat16_rn(y);
+    else static_cast<float*>(p.out)[o] = y;
 }
 
 // --------------------------------------------------------------------- few rows: stream
@@ -167,7 +161,7 @@ q8_stream_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
     if (warp == 0) {
         int stage = 0;
         uint32_t phase = 0;
-        for (long long u = first; u < units && !*abort_flag; u += step) {
+        for (long long u = first; u < units; u += step) {
             int g, row0, nrows;
             const int mt = unit(u, &g, &row0, &nrows);
             const int nl = (nrows + kSBox - 1) / kSBox;
@@ -240,14 +234,14 @@ q8_stream_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
     if (warp >= 2) {
         int acc = 0;
         uint32_t acc_phase = 0;
-        for (long long u = first; u < units && !*abort_flag; u += step) {
+        for (long long u = first; u < units; u += step) {
             int g, row0, nrows;
             const int mt = unit(u, &g, &row0, &nrows);
             const int wr = mt * kSWRows + r;
-            const bool wvalid = wr < p.N;   // N is even: a (gate, up) pair is valid or not as one
+            const bool wvalid = wr < p.N;
             float sw = 0.f, bias = 0.f;
             if (!SPLIT && wvalid) channel<MODE>(p, g, wr, &sw, &bias);
-            if (!mbar_wait(smem_u32(&tfull[acc]), acc_phase, abort_flag, kWaitNs)) break;
+            if (!mbar_wait_warp(smem_u32(&tfull[acc]), acc_phase, abort_flag, kWaitNs)) break;
             tc_fence_after();
             const uint32_t tb = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + static_cast<uint32_t>(acc * kSTok);
 #pragma unroll 1
@@ -344,6 +338,13 @@ q8_stream_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
 // itself cost 3000 cycles a unit (of 14800 at K = 2816, of 5900 at K = 704), the scales
 // loaded by the epilogue 4200.  16 warps of epilogue instead of 8 halve its time a unit (4900
 // -> 2200 cycles at N = 256): it waits for tensor memory and for stores, not for issue slots.
+// A slot (128 bytes of K: 16 KB of weights and up to 16 KB of tokens a CTA) takes 654 cycles
+// at N = 256 where its four MMAs take 512: an SM takes in about 50 bytes a cycle from L2.
+// Barriers a slot instead of two slots: 745 cycles.  Weight tiles kept in shared memory for
+// several token tiles change nothing at K = 704 (171.5 us against 175.5, 176.6 against
+// 175.9), where the stores of the outputs bound the unit.  Measured: 8191 rows, 4096 -> 4096,
+// 95 us (2896 TOP/s); E = 128, 65536 rows: 2816 -> 2 x 704 with SwiGLU 284 us, 704 -> 2816
+// 178 us (369 MB of outputs), the clock held to ~1.45 GHz by the power cap.
 constexpr int kPEpi = 16;
 constexpr int kPThreads = 128 + 32 * kPEpi;
 constexpr int kPPlan = 8;                // units worked out ahead
@@ -470,8 +471,8 @@ q8_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
                 const bool chunked = MODE == OUT_SWIGLU && p.chunked;
                 const int wc3 = chunked ? 0 : w_in / 32;
                 const int wc4 = chunked ? d.g * (p.N / 16) + w_in / 32 : d.g;
-                // the CTA's half of the tokens in boxes of 32 rows: the MMA's time goes by the
-                // shared memory's (operand reads and these writes), so no rows past the tile
+                // the CTA's half of the tokens in boxes of 32 rows: a slot's time goes by the
+                // bytes that come in, so no rows past the tile
                 const int nb = (unit_n(d.nrows) / 2 + kPBox - 1) / kPBox;
                 const uint32_t bytes = static_cast<uint32_t>(2 * (kPABytes + nb * kPBox * kBK));
                 bool ok = true;
@@ -503,7 +504,7 @@ q8_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
             uint32_t phase = 0, acc_phase = 0;
             auto rows_of_next = [&]() {   // the next unit's rows, 0 if the wait gave up
                 int n = 0;
-                if (mbar_wait(smem_u32(&ufull[plan.slot]), plan.phase, abort_flag, kWaitNs)) n = s_unit[plan.slot].nrows;
+                if (mbar_wait_warp(smem_u32(&ufull[plan.slot]), plan.phase, abort_flag, kWaitNs)) n = s_unit[plan.slot].nrows;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&uempty[plan.slot]));
                 plan.next();
@@ -515,14 +516,14 @@ q8_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
             const int steps = (p.K + 31) / 32;            // MMAs of a unit: none past K
             constexpr int kStep = kPSub * (kBK / 32);     // of a whole stage
             int nrows = pair < units ? rows_of_next() : 0, nrows_next = 0;
-            for (long long u = pair; u < units && !*abort_flag; u += npairs) {
+            for (long long u = pair; u < units && nrows > 0; u += npairs) {
                 const uint32_t idesc = idesc_s8_s32(2 * kPWRows, unit_n(nrows));
-                if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&tempty[acc]), acc_phase ^ 1u, abort_flag, kWaitNs))) break;
+                if (!mbar_wait_warp(smem_u32(&tempty[acc]), acc_phase ^ 1u, abort_flag, kWaitNs)) break;
                 tc_fence_after();
                 const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * kPAccCols);
                 bool ok = true;
                 for (int s0 = 0; s0 < steps; s0 += kStep) {
-                    if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&full[stage]), phase, abort_flag, kWaitNs))) {
+                    if (!mbar_wait_warp(smem_u32(&full[stage]), phase, abort_flag, kWaitNs)) {
                         ok = false;
                         break;
                     }
@@ -573,8 +574,8 @@ q8_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
         // ------------------------------------------------------------ scales, a unit ahead
         int acc = 0;
         uint32_t acc_phase = 0;
-        for (long long u = pair; u < units && !*abort_flag; u += npairs, plan.next()) {
-            if (!mbar_wait(smem_u32(&ufull[plan.slot]), plan.phase, abort_flag, kWaitNs)) break;
+        for (long long u = pair; u < units; u += npairs, plan.next()) {
+            if (!mbar_wait_warp(smem_u32(&ufull[plan.slot]), plan.phase, abort_flag, kWaitNs)) break;
             const PUnit d = s_unit[plan.slot];
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&uempty[plan.slot]));
@@ -587,7 +588,7 @@ q8_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
                 w8[i] = b8[i] = 0.f;
                 if (w0 + 32 * i < p.N) channel<MODE>(p, d.g, w0 + lane + 32 * i, &w8[i], &b8[i]);
             }
-            if (!mbar_wait(smem_u32(&sempty[acc]), acc_phase ^ 1u, abort_flag, kWaitNs)) break;
+            if (!mbar_wait_warp(smem_u32(&sempty[acc]), acc_phase ^ 1u, abort_flag, kWaitNs)) break;
             PScales& sc = s_scales[acc];
 #pragma unroll
             for (int i = 0; i < kPTok / 32; ++i) sc.sa[lane + 32 * i] = a8[i];
@@ -613,7 +614,7 @@ q8_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
         uint32_t acc_phase = 0;
         // the unit after the current one, read behind the current one's first loads
         auto read_unit = [&](PUnit* d) {
-            if (!mbar_wait(smem_u32(&ufull[plan.slot]), plan.phase, abort_flag, kWaitNs)) return false;
+            if (!mbar_wait_warp(smem_u32(&ufull[plan.slot]), plan.phase, abort_flag, kWaitNs)) return false;
             *d = s_unit[plan.slot];
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&uempty[plan.slot]));
@@ -622,14 +623,14 @@ q8_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
         };
         PUnit d, d_next{0, 0, 0, 0};
         bool ok = pair >= units || read_unit(&d);
-        for (long long u = pair; ok && u < units && !*abort_flag; u += npairs) {
+        for (long long u = pair; ok && u < units; u += npairs) {
             const int w0 = d.mt * 2 * kPWRows + static_cast<int>(rank) * kPWRows + quad * 32;
             const bool wvalid = w0 < p.N;   // N is a multiple of 32: the warp's rows are all valid or none
             const int wr = w0 + 4 * fj;
             constexpr int kChunks = kPTok / (32 * kParts);
-            if (!mbar_wait(smem_u32(&sfull[acc]), acc_phase, abort_flag, kWaitNs)) break;
+            if (!mbar_wait_warp(smem_u32(&sfull[acc]), acc_phase, abort_flag, kWaitNs)) break;
             const PScales& sc = s_scales[acc];
-            if (!mbar_wait(smem_u32(&tfull[acc]), acc_phase, abort_flag, kWaitNs)) break;
+            if (!mbar_wait_warp(smem_u32(&tfull[acc]), acc_phase, abort_flag, kWaitNs)) break;
             tc_fence_after();
             const uint32_t tb = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) +
                                 static_cast<uint32_t>(acc * kPAccCols);
@@ -764,8 +765,7 @@ cudaError_t launch_stream(const CUtensorMap& w, const CUtensorMap& x, const Q8Pa
     return launch_clusters(q8_stream_kernel<MODE, SPLIT>, clusters * cs, cs, kSThreads, stream_smem(SPLIT), s, w, x, p, cs);
 }
 
-// Pairs of CTAs that fit on the device at once, once per device (outside any capture: the
-// first call of a path runs before a graph is captured).
+// Pairs of CTAs that fit on the device at once, asked once per device.
 template <int MODE>
 cudaError_t max_pairs(int* pairs) {
     static int most[64] = {0};
@@ -813,7 +813,7 @@ constexpr int kStreamRows = 56;
 // Upper bound of the 64-row chunks: one per 64 rows, one more for every expert, at most one a
 // row (dense: exactly one per 64 rows).
 long long stream_units(const Q8GemmArgs& a) {
-    long long chunks = (a.rows + kSTok - 1) / kSTok;
+    long long chunks = (a.rows + kSTok - 1LL) / kSTok;
     if (a.offsets) chunks = a.rows < chunks + a.E ? a.rows : chunks + a.E;
     return chunks * ((a.N + kSWRows - 1) / kSWRows);
 }
@@ -843,7 +843,7 @@ cudaError_t product(const Q8GemmArgs& a, const Q8Params& p, cudaStream_t s) {
     if (MODE == OUT_SWIGLU || !use_stream(a)) {
         if (!tmap::quads8(&w, a.w_q, a.E, a.N, a.K, chunked)) return cudaErrorInvalidValue;
         if (!tmap::matrix8(&x, a.a_q, a.rows, a.K, kPBox, a.lda ? a.lda : a.K)) return cudaErrorInvalidValue;
-        const long long units = (static_cast<long long>((a.rows + kPTok - 1) / kPTok) + a.E) *
+        const long long units = ((a.rows + kPTok - 1LL) / kPTok + a.E) *
                                 ((a.N + 2 * kPWRows - 1) / (2 * kPWRows));
         return launch_pair<MODE>(w, x, p, units, s);
     }
