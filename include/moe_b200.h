@@ -260,7 +260,7 @@ moe_status moe_expert_ffn_q8(const void* x_perm, const int32_t* offsets, const i
  * scale 0 and q = 0; a row holding an infinity or a NaN has scale NaN and q = 0, so that
  * its products are NaN.
  *   x [rows, K] dt, K a multiple of 8; q [rows, K] int8 out; scale [rows] float32 out.
- * rows = 0 is a no-op. */
+ * rows = 0 is a no-op, more than 2^30 are refused (by the calls below as well). */
 moe_status moe_quantize_rows(const void* x, int rows, int K, moe_dtype dt, int8_t* q, float* scale,
                              void* stream);
 

@@ -123,14 +123,16 @@ constexpr int kQ8MaxK = 65536;
 constexpr int kMaxSequences = 65535;   // of the balance loss: one block each
 bool valid_q8_k(int K) { return K > 0 && K % 16 == 0 && K <= kQ8MaxK; }
 bool valid_q8_n(int N) { return N > 0 && N % 32 == 0; }
+bool valid_q8_rows(int rows) { return rows >= 0 && rows <= (1 << 30); }
 bool valid_w8a8_ffn(int H, int I) {
     return H > 0 && I > 0 && H % 32 == 0 && I % 32 == 0 && H <= kQ8MaxK && I <= kQ8MaxK;
 }
 
 // Workspace of the int8 expert FFN: error word and, for few rows per expert, the counters of
 // its one launch (both cleared by the row quantiser), the int8 rows and scales of x_perm,
-// the float32 activations, their int8 rows and scales.  The int8 rows start on 128-byte boundaries: a 128-byte slice of a row then lies in one line of
-// the L2 cache, which the loads of the products go by (rows of 704 bytes: two lines each).
+// the float32 activations, their int8 rows and scales.  The int8 rows start on 128-byte
+// boundaries: a 128-byte slice of a row then lies in one line of the L2 cache, which the
+// loads of the products go by (rows of 704 bytes: two lines each).
 struct W8a8Layout {
     size_t err, counters, clear_end, xq, xs, act, aq, as, total;
     int ldx, lda;   // bytes a row of xq, aq
@@ -738,7 +740,7 @@ moe_status moe_expert_ffn_q8(const void* x_perm, const int32_t* offsets, const i
 
 moe_status moe_quantize_rows(const void* x, int rows, int K, moe_dtype dt, int8_t* q, float* scale,
                              void* stream) {
-    if (rows < 0 || K <= 0 || K % 8 || !valid_dtype(dt)) return MOE_ERR_INVALID_ARG;
+    if (!valid_q8_rows(rows) || K <= 0 || K % 8 || !valid_dtype(dt)) return MOE_ERR_INVALID_ARG;
     if (rows == 0) return MOE_OK;
     if (!x || !q || !scale || !aligned(x, 16) || !aligned(q, 16) || !aligned(scale, 4))
         return MOE_ERR_INVALID_ARG;
@@ -757,7 +759,7 @@ moe_status moe_matmul_q8(const int8_t* a_q, const float* a_scale, const int8_t* 
                          const float* w_scale, const void* bias, const int32_t* offsets, int rows,
                          int K, int E, int N, moe_dtype out_dt, void* out, int32_t* err_word,
                          void* stream) {
-    if (rows < 0 || E <= 0 || E > kMaxExperts || !valid_q8_k(K) || !valid_q8_n(N) || !valid_dtype(out_dt) ||
+    if (!valid_q8_rows(rows) || E <= 0 || E > kMaxExperts || !valid_q8_k(K) || !valid_q8_n(N) || !valid_dtype(out_dt) ||
         (!offsets && E != 1))
         return MOE_ERR_INVALID_ARG;
     if (rows == 0) return MOE_OK;
@@ -785,7 +787,7 @@ moe_status moe_matmul_q8(const int8_t* a_q, const float* a_scale, const int8_t* 
 }
 
 size_t moe_expert_ffn_w8a8_workspace_size(int rows, int H, int E, int I) {
-    if (rows < 0 || E <= 0 || E > kMaxExperts || !valid_w8a8_ffn(H, I)) return 0;
+    if (!valid_q8_rows(rows) || E <= 0 || E > kMaxExperts || !valid_w8a8_ffn(H, I)) return 0;
     return w8a8_layout(rows, H, E, I).total;
 }
 
@@ -891,7 +893,7 @@ moe_status moe_expert_ffn_w8a8(const void* x_perm, const int32_t* offsets, const
                                const void* fc1_bias, const void* fc2_bias, int rows, int H, int E,
                                int I, moe_swiglu act, moe_fc1_layout fc1_layout, void* y_perm,
                                void* workspace, size_t ws_bytes, void* stream) {
-    if (rows < 0 || E <= 0 || E > kMaxExperts || !valid_w8a8_ffn(H, I) || !valid_swiglu(act) ||
+    if (!valid_q8_rows(rows) || E <= 0 || E > kMaxExperts || !valid_w8a8_ffn(H, I) || !valid_swiglu(act) ||
         !valid_layout(fc1_layout))
         return MOE_ERR_INVALID_ARG;
     if (rows == 0) return MOE_OK;

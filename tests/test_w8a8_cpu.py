@@ -158,6 +158,17 @@ def test_expert_ffn_w8a8_refusals():
     assert f(b1=ctypes.c_void_p(4097)) == INV
 
 
+def test_more_than_2_30_rows_are_refused():
+    """Row counts whose tiles and launch sizes would pass 32 bits."""
+    lib, many = _lib(), (1 << 30) + 1
+    assert lib.moe_quantize_rows(P, many, 64, 1, P, P, None) == INV
+    assert lib.moe_matmul_q8(P, P, P, P, None, P, many, 64, 2, 64, 1, P, None, None) == INV
+    assert lib.moe_expert_ffn_w8a8_workspace_size(many, 64, 2, 32) == 0
+    assert lib.moe_expert_ffn_w8a8_workspace_size(1 << 30, 64, 2, 32) > (1 << 30) * 64
+    assert lib.moe_expert_ffn_w8a8(P, P, P, P, P, P, None, None, many, 64, 2, 32, _abi.STANDARD_SWIGLU, 0, P, P,
+                                   (1 << 63) - 1, None) == INV
+
+
 def test_forward_w8a8_refusals():
     lib = _lib()
 
