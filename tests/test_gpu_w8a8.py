@@ -411,3 +411,75 @@ def test_binding_refuses_mismatches():
         moe.quantize_rows(torch.zeros(2, 12, device="cuda"))   # K not a multiple of 8
     with pytest.raises(moe.MoEError):
         moe.matmul_q8(q[:, :24].contiguous(), s, w[:, :24].contiguous(), sw)
+
+
+# The kernel of few rows, which runs the whole FFN in one launch: at fewer than 8 rows an
+# expert, and up to 48 where fc1 alone has more units of 256 weight rows than the chip has SMs.
+FEW = [  # rows, H, I, E, used, layout, act, biases
+    (12, 128, 64, 2, None, "interleaved", STD, False),
+    (20, 256, 128, 4, None, "chunked", OSS, True),
+    (900, 256, 96, 200, 3, "interleaved", STD, True),      # several chunks of one expert's tokens
+    (1500, 544, 416, 40, 2, "chunked", STD, False),        # more than 8 rows an expert, all in two
+    (1000, 160, 320, 50, 45, "interleaved", OSS, True),
+    (5, 32, 32, 256, None, "interleaved", STD, False),
+]
+
+
+@pytest.mark.parametrize("rows,H,I,E,used,layout,act,biases", FEW)
+def test_expert_ffn_w8a8_in_one_launch(rows, H, I, E, used, layout, act, biases):
+    x, xv, off, q1, s1, q2, s2, b1, b2 = _ffn_case(rows, H, I, E, used, biases, rows + I)
+    y = moe.expert_ffn_w8a8(x, dev(off), dev(q1), dev(s1), dev(q2), dev(s2), swiglu=act, fc1_layout=layout,
+                            fc1_bias=_dev_bias(b1), fc2_bias=_dev_bias(b2))
+    ref, bound = _ffn_ref(xv, off, q1, s1, q2, s2, b1[1], b2[1], layout, act)
+    check(from_dev(y), ref, bound, f"ffn {rows}x{H}x{I} E={E}")
+
+
+def test_few_rows_nan_row_and_zero_row():
+    rows, H, I, E = 14, 128, 64, 4
+    x, xv, off, q1, s1, q2, s2, _, _ = _ffn_case(rows, H, I, E, None, False, 20)
+    w = [dev(a) for a in (q1, s1, q2, s2)]
+    ref = moe.expert_ffn_w8a8(x, dev(off), *w)
+    x2 = x.clone()
+    x2[3, 5] = float("inf")
+    x2[9] = 0
+    y = moe.expert_ffn_w8a8(x2, dev(off), *w)
+    keep = [r for r in range(rows) if r not in (3, 9)]
+    assert torch.isnan(y[3].float()).all() and torch.all(y[9] == 0) and torch.equal(y[keep], ref[keep])
+
+
+@pytest.mark.parametrize("rows", [20, 400])
+def test_no_rows_in_any_expert(rows):
+    """Offsets that give no expert a row: nothing is written, no error."""
+    x, xv, off, q1, s1, q2, s2, _, _ = _ffn_case(rows, 128, 64, 4, None, False, 21)
+    w = [dev(a) for a in (q1, s1, q2, s2)]
+    nb = moe.expert_ffn_w8a8_workspace_size(rows, 128, 4, 64)
+    ws = torch.full((nb,), 0xA5, dtype=torch.uint8, device="cuda")
+    y = torch.full((rows, 128), 3.0, dtype=torch.bfloat16, device="cuda")
+    moe.expert_ffn_w8a8(x, torch.zeros(5, dtype=torch.int32, device="cuda"), *w, y_perm=y, workspace=ws)
+    assert moe.get_error(moe.workspace_error_word(ws)) == (_abi.MOE_OK, 0) and torch.all(y == 3.0)
+
+
+def test_few_rows_two_streams_and_graphs():
+    """The one-launch FFN on two streams at once, and two graphs that share a workspace."""
+    rows, H, I, E = 20, 512, 256, 4
+    x, xv, off, q1, s1, q2, s2, _, _ = _ffn_case(rows, H, I, E, None, False, 22)
+    w = [dev(a) for a in (q1, s1, q2, s2)]
+    o = dev(off)
+    want = {1: moe.expert_ffn_w8a8(x, o, *w), -1: moe.expert_ffn_w8a8(-x, o, *w)}
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    ys = [moe.expert_ffn_w8a8(x, o, *w, stream=streams[i % 2]) for i in range(20)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, want[1]) for y in ys)
+    xin, yout = torch.zeros_like(x), torch.zeros_like(x)
+    ws = torch.empty(moe.expert_ffn_w8a8_workspace_size(rows, H, E, I), dtype=torch.uint8, device="cuda")
+    graphs = [torch.cuda.CUDAGraph() for _ in range(2)]
+    for g in graphs:
+        with torch.cuda.graph(g):
+            for _ in range(3):   # calls in a row: each clears what the one before left
+                moe.expert_ffn_w8a8(xin, o, *w, y_perm=yout, workspace=ws)
+    for i in range(6):
+        sign = 1 if i % 2 == 0 else -1
+        xin.copy_(sign * x)
+        graphs[i % 2].replay()
+        assert torch.equal(yout, want[sign])
