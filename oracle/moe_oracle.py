@@ -64,7 +64,8 @@ notes of the repository):
   scale s[r]; its weights are q[r, :] * s[r] (symmetric, one scale per output row);
   the layer is the same layer on those weights.
 
-Parity pins for every function here live in tests/test_oracle_pins.py.  No
+Parity pins for every function here live in tests/test_oracle_pins.py; those of
+the int8 x int8 products and the balance loss in tests/test_w8a8_cpu.py.  No
 function in this file is "parity unpinned".
 """
 
