@@ -19,8 +19,9 @@
 // One pass over the row: a row's threads keep their vectors of 8 elements in registers
 // between the maximum and the rounding (rows longer than kRegVec vectors a thread read the
 // rest again, from L2).  Bound by HBM: rows K (2 or 4) bytes read, rows (K + 4) written.
-// Measured: 65536 x 2816 bf16 100 us, 5.5 TB/s (the quotient in float64: 309 us; a branch a
-// value for those near a half: 130 us).
+// Measured: 65536 x 2816 bf16 88 us, 6.3 TB/s; 65536 x 704 float32 38 us, 6.1 TB/s (65536 x
+// 2816 in an earlier form of 100 us: the quotient in float64 309 us, a branch a value for those
+// near a half 130 us).
 #include <type_traits>
 
 #include "common.cuh"
@@ -30,7 +31,16 @@
 namespace moe {
 namespace {
 
-constexpr int kQThreads = 256;
+constexpr int kMaxTpr = 256;
+// Threads of a block: 64 where a row's threads are no more, since a small block's registers
+// go to the next one as soon as its rows are out (blocks of 256: 65536 x 1536 float32 91 us
+// instead of 74, 65536 x 704 55 instead of 41).  Short float32 rows are held to 64 registers
+// a thread for more rows in flight (65536 x 704: 38 us; longer ones would spill, 74 -> 87 us).
+__host__ __device__ constexpr int block_threads(int tpr) { return tpr > 64 ? tpr : 64; }
+constexpr int kFew = 4;                  // vectors a thread of a short row
+__host__ __device__ constexpr int min_blocks(bool bf16, int tpr, int vec) {
+    return !bf16 && vec == kFew ? 1024 / block_threads(tpr) : 1;
+}
 
 template <bool BF16>
 struct Vec8 {
@@ -72,11 +82,11 @@ struct Vec8 {
 
 // TPR threads (a power of two, 32 .. 256) share a row, kRegVec vectors a thread in registers.
 template <bool BF16, int TPR, int kRegVec, bool SCATTER>
-__global__ void __launch_bounds__(kQThreads)
+__global__ void __launch_bounds__(block_threads(TPR), min_blocks(BF16, TPR, kRegVec))
 quantize_rows_kernel(const void* __restrict__ x, int rows, int K, int8_t* __restrict__ q, int ldq,
                      float* __restrict__ scale, const int32_t* __restrict__ perm_dst, int k, int rows_out,
                      int32_t* __restrict__ clear, int clear_words) {
-    constexpr int kRows = kQThreads / TPR;   // rows of a block
+    constexpr int kQThreads = block_threads(TPR), kRows = kQThreads / TPR;   // rows of a block
     __shared__ uint32_t s_max[kQThreads / 32];
     pdl_wait();
     pdl_trigger();
@@ -168,16 +178,16 @@ cudaError_t launch(const QuantizeArgs& a, cudaStream_t s) {
     const int rows = a.rows, K = a.K;
     const int nvec = K / 8;
     auto go = [&](auto kern, int tpr) {
-        const int per = kQThreads / tpr;
-        return launch_k(kern, dim3(static_cast<unsigned>((rows + per - 1) / per)), dim3(kQThreads), 0, s, a.x,
+        const int threads = block_threads(tpr), per = threads / tpr;
+        return launch_k(kern, dim3(static_cast<unsigned>((rows + per - 1) / per)), dim3(threads), 0, s, a.x,
                         rows, K, a.q, a.ldq ? a.ldq : K, a.scale, a.perm_dst, a.k, a.rows_out, a.clear, a.clear_words);
     };
     // Many rows: as few threads a row as hold it in registers, for many loads in flight and
-    // no barrier.  Few rows (less than four blocks an SM): spread a row, for latency.
-    constexpr int kReg = BF16 ? 12 : 6, kFew = 4;
+    // no barrier.  Few rows (less than 1024 threads an SM): spread a row, for latency.
+    constexpr int kReg = BF16 ? 12 : 6;
     const long long sms = device_sm_count();
     int tpr = 32;
-    while (tpr < kQThreads && (tpr * kReg < nvec || (tpr < nvec && static_cast<long long>(rows) * tpr < 4 * kQThreads * sms)))
+    while (tpr < kMaxTpr && (tpr * kReg < nvec || (tpr < nvec && static_cast<long long>(rows) * tpr < 1024 * sms)))
         tpr *= 2;
     const bool few = tpr * kFew >= nvec;
     auto pick = [&](auto scatter) {
