@@ -18,8 +18,8 @@
 // A row's E logits are spread over LPR lanes with 8 each (two 16-byte vectors where E is a
 // multiple of 4), 32 / LPR rows to a warp, the loads of the next two rows issued before the
 // current one is used.  Bound by HBM: 4 T E bytes read, the gradient as much again and written.
-// Measured, 131071 x 256, k = 8: forward 36 us (141 MB of logits, ids and mask, 6 us of it the second
-// launch), gradient 49 us (268 MB, 5.5 TB/s).
+// Measured, 131071 x 256, k = 8: forward 38 us (138 MB of logits, ids and mask; 6 us of it the
+// second launch), gradient 49 us (268 MB, 5.5 TB/s).
 #include <type_traits>
 
 #include "common.cuh"
