@@ -483,3 +483,24 @@ def test_few_rows_two_streams_and_graphs():
         xin.copy_(sign * x)
         graphs[i % 2].replay()
         assert torch.equal(yout, want[sign])
+
+
+@pytest.mark.parametrize("rows,H,I,E,empty", [(25, 256, 96, 3, 9), (100, 352, 160, 4, 30), (700, 64, 224, 2, 150)])
+def test_experts_without_rows_change_nothing(rows, H, I, E, empty):
+    """The same rows with and without experts that get none: other kernels (the launches of
+    many rows per expert, the one of few), the same bits."""
+    x, _, off, q1, s1, q2, s2, b1, b2 = _ffn_case(rows, H, I, E, None, True, 23)
+    w = [dev(a) for a in (q1, s1, q2, s2)]
+    want = moe.expert_ffn_w8a8(x, dev(off), *w, swiglu=OSS, fc1_bias=b1[0].cuda(), fc2_bias=b2[0].cuda())
+
+    def spread(t):   # every expert behind `empty` / E others of the same size
+        out = torch.ones((E, empty // E + 1) + t.shape[1:], dtype=t.dtype, device="cuda")
+        out[:, -1] = t
+        return out.flatten(0, 1).contiguous()
+    step = empty // E + 1
+    many = np.concatenate([[0], np.repeat(off[1:], step)])
+    for e in range(E):
+        many[1 + e * step:1 + (e + 1) * step - 1] = off[e]
+    y = moe.expert_ffn_w8a8(x, dev(many.astype(np.int32)), *[spread(t) for t in w], swiglu=OSS,
+                            fc1_bias=spread(b1[0].cuda()), fc2_bias=spread(b2[0].cuda()))
+    assert torch.equal(y, want)
