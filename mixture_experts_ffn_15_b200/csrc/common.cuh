@@ -73,11 +73,24 @@ struct SwigluAttr {
     int standard;
 };
 
+// min and max that carry a NaN on (fminf and fmaxf drop it: a NaN row would leave a clipped
+// activation as an ordinary number).
+__device__ __forceinline__ float min_nan(float a, float b) {
+    float d;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+
 __device__ __forceinline__ float swiglu_attr(float g, float u, const SwigluAttr& a) {
     if (a.standard) return swiglu_f32(g, u);
     if (a.limit < INFINITY) {
-        g = fminf(g, a.limit);
-        u = fminf(fmaxf(u, -a.limit), a.limit);
+        g = min_nan(g, a.limit);
+        u = min_nan(max_nan(u, -a.limit), a.limit);
     }
     return g / (1.0f + expf(-a.alpha * g)) * (u + a.beta);
 }
@@ -85,8 +98,8 @@ __device__ __forceinline__ float swiglu_attr(float g, float u, const SwigluAttr&
 __device__ __forceinline__ float swiglu_attr_fast(float g, float u, const SwigluAttr& a) {
     if (a.standard) return swiglu_fast(g, u);
     if (a.limit < INFINITY) {
-        g = fminf(g, a.limit);
-        u = fminf(fmaxf(u, -a.limit), a.limit);
+        g = min_nan(g, a.limit);
+        u = min_nan(max_nan(u, -a.limit), a.limit);
     }
     return __fdividef(g, 1.0f + __expf(-a.alpha * g)) * (u + a.beta);
 }
