@@ -90,7 +90,10 @@ quantize_rows_kernel(const void* __restrict__ x, int rows, int K, int8_t* __rest
     __shared__ uint32_t s_max[kQThreads / 32];
     pdl_wait();
     pdl_trigger();
-    for (int i = blockIdx.x * kQThreads + threadIdx.x; i < clear_words; i += gridDim.x * kQThreads) clear[i] = 0;
+    // 64 bits: 2^30 rows make more than 2^31 threads
+    for (long long i = static_cast<long long>(blockIdx.x) * kQThreads + threadIdx.x; i < clear_words;
+         i += static_cast<long long>(gridDim.x) * kQThreads)
+        clear[i] = 0;
     const int nvec = K / 8;
     const int t = threadIdx.x % TPR;
     const long long row = static_cast<long long>(blockIdx.x) * kRows + threadIdx.x / TPR;

@@ -58,3 +58,20 @@ def test_a_nan_row_of_the_weight_only_int8_ffn_comes_out_nan():
     y = moe.expert_ffn_q8(x, *args, swiglu=OSS)
     keep = [r for r in range(rows) if r != 3]
     assert torch.isnan(y[3].float()).all() and torch.equal(y[keep], ref[keep])
+
+
+def test_quantize_rows_of_more_than_2_31_threads():
+    """2^26 + 3 rows of 8 values: 32 threads a row, so that the thread numbers pass 31 bits."""
+    rows, K, step = (1 << 26) + 3, 8, 1 << 23
+    g = torch.Generator(device="cuda").manual_seed(33)
+    x = torch.empty((rows, K), dtype=torch.bfloat16, device="cuda")
+    for a in range(0, rows, step):
+        x[a:a + step].normal_(generator=g)
+    q, s = moe.quantize_rows(x)
+    for a in range(0, rows, step):
+        v = x[a:a + step].double()
+        top = v.abs().amax(1, keepdim=True)
+        # by a tensor: torch multiplies by the reciprocal of a Python number
+        assert torch.equal(s[a:a + step], top[:, 0].float() / torch.full_like(s[a:a + step], 127))
+        # 127 v is exact in float64, the quotient is a half exactly or far from one
+        assert torch.equal(q[a:a + step], (127 * v / top.clamp_min(1e-300)).round().to(torch.int8))
