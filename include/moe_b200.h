@@ -331,7 +331,7 @@ moe_status moe_forward_w8a8(const void* hidden, const void* norm_weight, float n
  *   loss [1], counts [S, E] int32, probs [S, E] float32 (P), tokens [S] int32 (n): out
  *   err_word    int32 device word or NULL: MOE_DEVERR_BAD_EXPERT is OR-ed in for an id
  *               outside [0, E) (it is left out of the counts) or bad sequence offsets
- *               (clamped to [0, T])
+ *               (clamped to [0, T]; one below an earlier one counts as that one)
  *   workspace   at least moe_balance_loss_workspace_size(T, E, S) bytes, 256-byte aligned,
  *               any contents
  * A logit of -infinity has probability 0; a token whose logits are all -infinity has no

@@ -35,19 +35,29 @@ constexpr int kPer = 8;                  // logits a lane holds
 constexpr int kTokensPerBlockMin = 64;
 constexpr int kOneBlockTokens = 256;     // up to here one block takes the batch
 
-// Sequence bounds with offsets clamped to [0, T] (nullptr: one sequence, the batch).
-__device__ __forceinline__ int seq_bound(const int32_t* seq, int s, int T) {
+// Sequence s is the tokens [M_s, M_{s+1}) with M_i the largest of the offsets 0 .. i, each
+// clamped to [0, T]: offsets that decrease make empty sequences, and every token lies in one
+// sequence at most whatever the offsets hold.  Valid offsets are their own M.
+
+// Offset s clamped to [0, T] (nullptr: one sequence, the batch).
+__device__ __forceinline__ int seq_offset(const int32_t* seq, int s, int T) {
     return seq ? min(max(seq[s], 0), T) : (s == 0 ? 0 : T);
 }
 
-// Last sequence whose first token is at or before t (0 if none is).
-__device__ __forceinline__ int seq_at(const int32_t* seq, int S, int t, int T) {
-    int lo = 0, hi = S - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (seq_bound(seq, mid, T) <= t) lo = mid; else hi = mid - 1;
-    }
-    return lo;
+// First i with M_i >= t (the first offset that is), S + 1 if there is none; by the whole block.
+__device__ __forceinline__ int first_bound(const int32_t* seq, int S, int t, int T, int* s_first) {
+    if (t <= 0) return 0;
+    if (!seq) return t <= T ? 1 : 2;
+    if (threadIdx.x == 0) *s_first = S + 1;
+    __syncthreads();
+    int at = S + 1;
+#pragma unroll 4
+    for (int i = threadIdx.x; i <= S; i += blockDim.x)
+        if (seq_offset(seq, i, T) >= t) at = min(at, i);
+    at = __reduce_min_sync(0xffffffffu, at);
+    if ((threadIdx.x & 31) == 0 && at <= S) atomicMin(s_first, at);
+    __syncthreads();
+    return *s_first;
 }
 
 // The 8 logits of lane l (of LPR) of a row: with VEC, experts 4 l .. 4 l + 3 and
@@ -121,6 +131,7 @@ struct BalanceParams {
     const int32_t* seq;
     int T, E, k, S, per_block, blocks;
     float coef;
+    int32_t* bounds;       // [S + 1], M above; not used without seq
     float* part_p;         // [blocks + S, E]
     int32_t* part_c;       // [blocks + S, E]
     int32_t* part_n;       // [blocks + S]
@@ -162,7 +173,7 @@ balance_partial_kernel(const BalanceParams p) {
     constexpr int kRows = 32 / LPR;     // rows of a warp
     __shared__ float s_p[kBWarps][kMaxExperts];
     __shared__ int s_c[kMaxExperts];
-    __shared__ int s_n;
+    __shared__ int s_n, s_first;
     __shared__ double s_red[kBWarps];
     pdl_wait();
     pdl_trigger();
@@ -182,10 +193,22 @@ balance_partial_kernel(const BalanceParams p) {
     const int t0 = static_cast<int>(min(static_cast<long long>(b) * p.per_block, static_cast<long long>(T)));
     const int t1 = static_cast<int>(min(static_cast<long long>(t0) + p.per_block, static_cast<long long>(T)));
     const bool single = p.blocks <= 1 && S == 1;   // one block finishes the batch
-    for (int s = seq_at(p.seq, S, t0, T); s < S; ++s) {
-        const int lo = seq_bound(p.seq, s, T);
-        if (lo >= t1 && !single) break;
-        const int a = max(lo, t0), z = min(seq_bound(p.seq, s + 1, T), t1);
+    // The walk starts with the sequence before the first bound in the range (its own bound is
+    // smaller: lo = t0 stands for it).  The block that holds a bound writes it for the second
+    // launch, the last block those at T as well.
+    const bool last = b == static_cast<int>(gridDim.x) - 1, note = p.seq && !single;
+    const int i0 = first_bound(p.seq, S, t0, T, &s_first);
+    int lo = i0 == 0 ? seq_offset(p.seq, 0, T) : t0, hi = lo;
+    if (note && i0 == 0 && threadIdx.x == 0 && lo < t1) p.bounds[0] = lo;
+    for (int s = max(i0 - 1, 0); s < S; ++s, lo = hi) {
+        if (lo >= t1 && !single) {
+            if (note && last)   // lo = T: every bound from here on is
+                for (int i = s + threadIdx.x; i <= S; i += kBThreads) p.bounds[i] = T;
+            break;
+        }
+        hi = max(lo, seq_offset(p.seq, s + 1, T));
+        if (note && threadIdx.x == 0 && hi >= t0 && (hi < t1 || last)) p.bounds[s + 1] = hi;
+        const int a = max(lo, t0), z = min(hi, t1);
         if (a >= z && !single) continue;
         for (int e = threadIdx.x; e < E; e += kBThreads) s_c[e] = 0;
         if (threadIdx.x == 0) s_n = 0;
@@ -284,7 +307,7 @@ balance_reduce_kernel(const BalanceParams p) {
     __syncthreads();
     const int s = blockIdx.x, E = p.E, nb = gridDim.y;
     const int e = static_cast<int>(blockIdx.y) * kRExperts + (threadIdx.x & 31), st = threadIdx.x >> 5;
-    const int lo = seq_bound(p.seq, s, p.T), hi = seq_bound(p.seq, s + 1, p.T);
+    const int lo = p.seq ? p.bounds[s] : 0, hi = p.seq ? p.bounds[s + 1] : p.T;
     const int b0 = lo / p.per_block, b1 = hi > lo ? (hi - 1) / p.per_block + 1 : b0;
     int n = 0;
     for (int b = b0 + threadIdx.x; b < b1; b += kBThreads) n += p.part_n[b + s];
@@ -343,9 +366,14 @@ balance_grad_kernel(const BalanceGradArgs a, int per_block) {
     const int t0 = static_cast<int>(min(static_cast<long long>(blockIdx.x) * per_block, static_cast<long long>(T)));
     const int t1 = static_cast<int>(min(static_cast<long long>(t0) + per_block, static_cast<long long>(T)));
     int t = t0 + warp * kRows + sub;
-    // the lane group's sequence: its bounds, shares less 1/E and scale; t only grows
-    int s = seq_at(a.seq_offsets, a.S, min(t, T - 1), T);
-    int lo = seq_bound(a.seq_offsets, s, T), hi = seq_bound(a.seq_offsets, s + 1, T);
+    // the lane group's sequence: its bounds (M), shares less 1/E and scale; t only grows.  It
+    // starts with the block's first token: the sequence before the first bound behind t0
+    // (whose own bound is at or before t0: lo = t0 stands for it), or none.
+    __shared__ int s_first;
+    const int i1 = first_bound(a.seq_offsets, a.S, t0 + 1, T, &s_first);
+    int s = min(max(i1 - 1, 0), a.S - 1);
+    int lo = i1 == 0 ? seq_offset(a.seq_offsets, 0, T) : t0;
+    int hi = i1 > a.S ? t0 : max(lo, seq_offset(a.seq_offsets, s + 1, T));
     int have = -1;
     float f[kPer], scale = 0.f;
 #pragma unroll
@@ -365,7 +393,7 @@ balance_grad_kernel(const BalanceGradArgs a, int per_block) {
         while (t >= hi && s + 1 < a.S && t < t1) {
             ++s;
             lo = hi;
-            hi = seq_bound(a.seq_offsets, s + 1, T);
+            hi = max(lo, seq_offset(a.seq_offsets, s + 1, T));
         }
         const bool live = t < t1 && m != 0 && t >= lo && t < hi;
         if (live && s != have) {
@@ -404,7 +432,7 @@ size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
 struct BalanceLayout {
     int blocks, per_block;
-    size_t ticket, seq_loss, part_n, part_c, part_p, total;
+    size_t ticket, bounds, seq_loss, part_n, part_c, part_p, total;
 };
 
 BalanceLayout balance_layout(int T, int E, int S) {
@@ -416,7 +444,8 @@ BalanceLayout balance_layout(int T, int E, int S) {
     L.blocks = (T + L.per_block - 1) / L.per_block;
     const size_t slots = static_cast<size_t>(L.blocks) + S;
     L.ticket = 0;
-    L.seq_loss = 256;
+    L.bounds = 256;
+    L.seq_loss = L.bounds + align256((static_cast<size_t>(S) + 1) * 4);
     L.part_n = L.seq_loss + align256(static_cast<size_t>(S) * ((E + kRExperts - 1) / kRExperts) * 8);
     L.part_c = L.part_n + align256(slots * 4);
     L.part_p = L.part_c + align256(slots * E * 4);
@@ -448,7 +477,7 @@ cudaError_t launch_balance_loss(const BalanceArgs& a, cudaStream_t s) {
     const BalanceLayout L = balance_layout(a.T, a.E, a.S);
     char* ws = static_cast<char*>(a.workspace);
     const BalanceParams p{a.logits, a.topk_idx, a.mask, a.seq_offsets, a.T, a.E, a.k, a.S, L.per_block, L.blocks,
-                          a.coef, reinterpret_cast<float*>(ws + L.part_p), reinterpret_cast<int32_t*>(ws + L.part_c),
+                          a.coef, reinterpret_cast<int32_t*>(ws + L.bounds), reinterpret_cast<float*>(ws + L.part_p), reinterpret_cast<int32_t*>(ws + L.part_c),
                           reinterpret_cast<int32_t*>(ws + L.part_n), reinterpret_cast<int32_t*>(ws + L.ticket),
                           reinterpret_cast<double*>(ws + L.seq_loss), a.loss, a.counts, a.probs, a.tokens, a.err};
     const dim3 grid(L.blocks > 0 ? L.blocks : 1), block(kBThreads);

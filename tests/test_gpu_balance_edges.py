@@ -1,0 +1,54 @@
+"""The balance loss on the GPU where its ranges, sequences and sums are at their worst:
+offsets that decrease, blocks that walk many rows, very many tokens.  Bounds: test_gpu_balance."""
+import numpy as np
+import pytest
+import torch
+
+import mixture_experts_ffn_15_b200 as moe
+from mixture_experts_ffn_15_b200 import _abi
+from test_gpu_balance import compare, run
+
+pytestmark = pytest.mark.gpu
+
+
+def batch(T, E, k, seed):
+    rng = np.random.default_rng(seed)
+    lg = (rng.standard_normal((T, E)) * 2 + rng.standard_normal(E)).astype(np.float32).astype(np.float64)
+    return lg, np.argsort(-lg, axis=1, kind="stable")[:, :k], rng
+
+
+def poisoned(T, E, S):
+    n = moe.load_library().moe_balance_loss_workspace_size(T, E, S)
+    return torch.full((n,), 0xFF, dtype=torch.uint8, device="cuda")
+
+
+@pytest.mark.parametrize("T,seqs", [
+    (40, [[0, 20, 10, 40], [5, 40], [30, 10, 40], [0, 50], [-5, 40], [40, 0], [90, 95, 100], [40, 40, 3]]),
+    (1000, [[0, 600, 300, 700, 650, 1000], [700, 100, 900, 200, 1000], [0, 5000, 20, 30], [300, 1000, 0, 1000],
+            [1000, 0, 0, 0], [0, 64, 128, 64, 64, 192, 128, 900], [-7, 63, -8, 65, 2000], [999, 1000, 1000, 5]]),
+    (12000, [[0, 9000, 30, 9001, 11000, 200, 12000], [11999, 12000, 1], [0] + [7000, 100] * 600 + [12000]])])
+def test_offsets_that_decrease_make_empty_sequences(T, seqs):
+    """The offsets count as their running maximum, clamped to the batch; never-written memory
+    has no part in the results; the error word tells."""
+    lg, idx, rng = batch(T, 12, 2, T)
+    mask = rng.random(T) < 0.8
+    for seq in seqs:
+        bounds = np.maximum.accumulate(np.clip(seq, 0, T))
+        err = torch.zeros(1, dtype=torch.int32, device="cuda")
+        got = run(lg, idx, 0.5, mask, seq, err_word=err, workspace=poisoned(T, 12, len(seq) - 1))
+        compare(got, lg, idx, 0.5, mask, bounds)
+        assert moe.get_error(err) == (_abi.MOE_ERR_DEVICE, 1), seq
+
+
+@pytest.mark.parametrize("T,S", [(1, 3000), (700, 2500), (3000, 3000), (40000, 1500), (0, 5)])
+def test_many_sequences(T, S):
+    """More sequences than a block has threads, most of them empty or of a few tokens."""
+    lg, idx, rng = batch(T, 8, 2, S)
+    seq = np.concatenate([[0], np.sort(rng.integers(0, T + 1, S - 1)), [T]])
+    if T == 700:
+        seq = np.minimum(np.arange(S + 1) // 3, T)   # empty ones between all the others
+        seq[-1] = T
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = run(lg, idx, 1.0, None, seq, err_word=err, workspace=poisoned(T, 8, S))
+    compare(got, lg, idx, 1.0, None, seq)
+    assert moe.get_error(err) == (_abi.MOE_OK, 0)
