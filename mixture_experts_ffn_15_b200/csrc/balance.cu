@@ -9,7 +9,7 @@
 // are close to 1/E and their difference would lose its leading digits.  (c_e E - n k is
 // formed in whole numbers, so the difference itself is exact.)
 //
-// Forward: B blocks take equal ranges of tokens; a block writes one row of partial sums
+// Forward: the blocks take equal ranges of tokens; a block writes one row of partial sums
 // and counts for every sequence that its range meets, into slot b + s (walking along the
 // tokens either the block or the sequence advances, so slots are unique).  A second launch
 // adds each sequence's slots in order: no floating-point atomics, the same bits every time.
@@ -37,6 +37,8 @@ constexpr int kGThreads = 384;           // two blocks an SM at 80 registers
 constexpr int kPer = 8;                  // logits a lane holds
 constexpr int kTokensPerBlockMin = 64;
 constexpr int kOneBlockTokens = 256;     // up to here one block takes the batch
+constexpr int kFold = 32;                // rows a lane adds up before it adds the sum to its longer one
+constexpr int kMostRows = kFold * kFold; // rows a lane takes
 
 // Sequence s is the tokens [M_s, M_{s+1}) with M_i the largest of the offsets 0 .. i, each
 // clamped to [0, T]: offsets that decrease make empty sequences, and every token lies in one
@@ -174,7 +176,8 @@ template <int LPR, bool VEC, bool RAGGED>
 __global__ void __launch_bounds__(kBThreads, 1)
 balance_partial_kernel(const BalanceParams p) {
     constexpr int kRows = 32 / LPR;     // rows of a warp
-    __shared__ float s_p[kBWarps][kMaxExperts];
+    __shared__ float s_p[kBWarps][kMaxExperts];   // folded sums of the lanes, then sums of the warps
+    static_assert(kMaxExperts == 32 * kPer, "a warp's folded sums");
     __shared__ int s_c[kMaxExperts];
     __shared__ int s_n, s_first;
     __shared__ double s_red[kBWarps];
@@ -258,6 +261,18 @@ balance_partial_kernel(const BalanceParams p) {
             m1 = m2;
             r = next;
             next = next2;
+            if (it % kFold == kFold - 1) {
+#pragma unroll
+                for (int i = 0; i < kPer; ++i) {
+                    s_p[warp][32 * i + lane] = (it < kFold ? 0.f : s_p[warp][32 * i + lane]) + acc[i];
+                    acc[i] = 0.f;
+                }
+            }
+        }
+        if (trips >= kFold) {
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) acc[i] += s_p[warp][32 * i + lane];
+            __syncwarp();
         }
         // the warp's rows, then the warps, in order
 #pragma unroll
@@ -444,9 +459,23 @@ struct BalanceLayout {
     size_t ticket, bounds, seq_loss, part_n, part_c, part_p, total;
 };
 
+// Lanes of a row: the smallest power of two that holds E logits at 8 a lane.
+int lanes_per_row(int E) {
+    int n = 1;
+    while (n * kPer < E) n *= 2;
+    return n;
+}
+
+// One block an SM, as many times over as it takes for ranges of at most kMostRows rows a lane.
+// With the sums folded every kFold rows, a float32 probability goes through at most 31 + 32
+// additions of a lane, 5 of the lanes and 31 of the warps in front of the second launch's
+// float64, whatever T is.  (400000 x 256 forward: 88 us, one long sum a lane 86, ranges of
+// kFold rows instead 97.)
 BalanceLayout balance_layout(int T, int E, int S) {
     BalanceLayout L;
-    const int most = 148;
+    const int sms = 148, range = kMostRows * kBWarps * (32 / lanes_per_row(E));
+    const int each = (T + sms - 1) / sms;
+    const int most = sms * (each > range ? (each + range - 1) / range : 1);
     L.per_block = (T + most - 1) / most;
     if (L.per_block < kTokensPerBlockMin) L.per_block = kTokensPerBlockMin;
     if (T <= kOneBlockTokens) L.per_block = kOneBlockTokens;
@@ -462,7 +491,7 @@ BalanceLayout balance_layout(int T, int E, int S) {
     return L;
 }
 
-// fn(lanes per row, vector loads) with the smallest LPR that holds E logits at 8 a lane.
+// fn(lanes per row, vector loads).
 template <typename F>
 cudaError_t by_experts(int E, F fn) {
     const bool vec = E % 4 == 0;
@@ -470,12 +499,14 @@ cudaError_t by_experts(int E, F fn) {
         constexpr int L = decltype(lpr)::value;
         return vec ? fn(lpr, std::true_type()) : fn(std::integral_constant<int, L>(), std::false_type());
     };
-    if (E <= 8) return go(std::integral_constant<int, 1>());
-    if (E <= 16) return go(std::integral_constant<int, 2>());
-    if (E <= 32) return go(std::integral_constant<int, 4>());
-    if (E <= 64) return go(std::integral_constant<int, 8>());
-    if (E <= 128) return go(std::integral_constant<int, 16>());
-    return go(std::integral_constant<int, 32>());
+    switch (lanes_per_row(E)) {
+        case 1: return go(std::integral_constant<int, 1>());
+        case 2: return go(std::integral_constant<int, 2>());
+        case 4: return go(std::integral_constant<int, 4>());
+        case 8: return go(std::integral_constant<int, 8>());
+        case 16: return go(std::integral_constant<int, 16>());
+        default: return go(std::integral_constant<int, 32>());
+    }
 }
 
 }  // namespace

@@ -52,3 +52,50 @@ def test_many_sequences(T, S):
     got = run(lg, idx, 1.0, None, seq, err_word=err, workspace=poisoned(T, 8, S))
     compare(got, lg, idx, 1.0, None, seq)
     assert moe.get_error(err) == (_abi.MOE_OK, 0)
+
+
+def test_probabilities_of_very_many_tokens():
+    """Every row the same, its probabilities such that each float32 addition of a long sum
+    rounds the same way (1000 of them in a row: 230 U32 off).  Bound: (18 + 2.3 |logit - max|)
+    U32 of a probability, 31 + 32 additions of a lane, 5 of the lanes, 31 of the warps, the
+    result's rounding: 119 U32."""
+    T, E, x = 148 * 32 * 1000 + 5, 160, 0.101
+    row = torch.zeros(E, dtype=torch.float32, device="cuda")
+    row[7] = x
+    logits = row.expand(T, E).contiguous()
+    idx = torch.arange(T, dtype=torch.int32, device="cuda").remainder(E)[:, None].contiguous()
+    r = moe.balance_loss(logits, idx, coef=1.0)
+    p = torch.softmax(row.double(), 0)
+    U32 = 2.0 ** -24
+    assert torch.all((r["probs"][0].double() - p).abs() <= 119 * U32 * p)
+    assert torch.equal(r["counts"][0].long(), torch.bincount(idx[:, 0], minlength=E))
+    loss = float(E * (r["counts"][0].double() / T * p).sum())
+    assert abs(float(r["loss"]) - loss) <= 121 * U32 * loss      # its sum in float64, one rounding
+    d = moe.balance_loss_backward(logits, 1, r["counts"], r["tokens"])
+    assert torch.equal(d, d[:1].expand(T, E))                   # equal rows, equal bits
+
+
+@pytest.mark.parametrize("E", [1, 8, 9, 60, 130])
+def test_long_ranges(E):
+    """T where a lane folds its sums several times, for each number of lanes; with E = 130, T
+    where a block's range passes its largest number of rows.  Bound: (18 + 2.3 |logit - max|)
+    U32 with the maximum at most 9 above, 31 + 16 + 5 + 31 additions, one rounding: 123 U32."""
+    lanes = 1
+    while lanes * 8 < E:
+        lanes *= 2
+    T = 148 * 32 * (1024 if E > 60 else 65) * (32 // lanes) + 3
+    g = torch.Generator(device="cuda").manual_seed(E)
+    logits = torch.randn((T, E), generator=g, device="cuda")
+    mask = torch.rand((T,), generator=g, device="cuda") < 0.9
+    seq = torch.tensor([0, T // 3, T // 3, T - 1], dtype=torch.int32, device="cuda")
+    idx = logits.argmax(1, keepdim=True).int()
+    r = moe.balance_loss(logits, idx, mask=mask, seq_offsets=seq)
+    p = torch.softmax(logits.double(), 1)
+    for s in range(3):
+        a, z = int(seq[s]), int(seq[s + 1])
+        m = mask[a:z]
+        n = int(m.sum())
+        assert int(r["tokens"][s]) == n
+        assert torch.equal(r["counts"][s].long(), torch.bincount(idx[a:z, 0][m], minlength=E))
+        want = p[a:z][m].sum(0) / max(n, 1)
+        assert torch.all((r["probs"][s].double() - want).abs() <= 128 * 2.0 ** -24 * want)
