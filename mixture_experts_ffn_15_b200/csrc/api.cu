@@ -128,9 +128,10 @@ bool valid_w8a8_ffn(int H, int I) {
     return H > 0 && I > 0 && H % 32 == 0 && I % 32 == 0 && H <= kQ8MaxK && I <= kQ8MaxK;
 }
 
-// Workspace of the int8 expert FFN: error word and, for few rows per expert, the counters of
-// its one launch (both cleared by the row quantiser), the int8 rows and scales of x_perm,
-// the float32 activations, their int8 rows and scales.  The int8 rows start on 128-byte
+// Workspace of the int8 expert FFN: error word and the counters of the one launch for few rows
+// per expert (both cleared by the row quantiser), the int8 rows and scales of x_perm, the
+// float32 activations, their int8 rows and scales.  The counters keep their place where that
+// launch does not run, so that a workspace for more rows holds fewer rows too.  The int8 rows start on 128-byte
 // boundaries: a 128-byte slice of a row then lies in one line of the L2 cache, which the
 // loads of the products go by (rows of 704 bytes: two lines each).
 struct W8a8Layout {
@@ -143,8 +144,8 @@ W8a8Layout w8a8_layout(int rows, int H, int E, int I) {
     Carver c;
     W8a8Layout L;
     L.err = c.take(kAlign);
-    L.counters = c.take(q8_ffn_supported(rows, E, I) ? static_cast<size_t>(q8_ffn_counters(rows, E)) * 4 : 0);
-    L.clear_end = c.off;
+    L.counters = c.take(static_cast<size_t>(q8_ffn_counters(rows, E)) * 4);
+    L.clear_end = q8_ffn_supported(rows, E, I) ? c.off : L.counters;
     L.ldx = (H + 127) / 128 * 128;
     L.lda = (I + 127) / 128 * 128;
     L.xq = c.take(r * L.ldx);

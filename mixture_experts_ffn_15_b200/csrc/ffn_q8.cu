@@ -546,13 +546,18 @@ q8_ffn_kernel(const __grid_constant__ CUtensorMap tmW1, const __grid_constant__ 
 // 239.0 / 193.7; E = 32, H = 1024, I = 512 (128 units): 4 rows per expert 24.7 / 24.9, 32 per
 // expert 37.2 / 26.8; E = 8, H = 2816, I = 704: 1 row per expert 24.9 / 25.1, 32 per expert
 // 35.2 / 29.3.
+constexpr int kMostPerExpert = 48;
+
 bool q8_ffn_supported(int rows, int E, int I) {
     const long long r = rows;
-    return r <= 48LL * E && (r < 8LL * E || static_cast<long long>(E) * ((2 * I + 255) / 256) > 148);
+    return r <= static_cast<long long>(kMostPerExpert) * E && (r < 8LL * E || static_cast<long long>(E) * ((2 * I + 255) / 256) > 148);
 }
 
-// Two words per chunk and the scheduler's.
-int q8_ffn_counters(int rows, int E) { return 2 * (rows / kTok + E + 1) + 1; }
+// Two words per chunk and the scheduler's; for more rows than the kernel takes, those of the most.
+int q8_ffn_counters(int rows, int E) {
+    const int most = kMostPerExpert * E;
+    return 2 * ((rows < most ? rows : most) / kTok + E + 1) + 1;
+}
 
 cudaError_t launch_q8_ffn(const Q8FfnArgs& a, cudaStream_t s) {
     if (a.rows <= 0) return cudaSuccess;

@@ -1,0 +1,28 @@
+"""int8 products and balance loss without a GPU: workspace sizes over whole ranges, refusals."""
+import pytest
+
+from mixture_experts_ffn_15_b200 import _abi
+from mixture_experts_ffn_15_b200.build import build
+
+
+def _lib():
+    build()
+    return _abi.load()
+
+
+def never_shrinks(size, values):
+    last = 0
+    for v in values:
+        n = size(v)
+        assert n > 0 and n >= last, (v, n, last)
+        last = n
+
+
+@pytest.mark.parametrize("H,E,I", [(128, 128, 64), (128, 256, 64), (32, 1, 32), (64, 200, 96), (2816, 8, 704)])
+def test_a_workspace_of_the_ffn_holds_fewer_rows_too(H, E, I):
+    """Also across the row counts at which other kernels take over (8 and 48 per expert)."""
+    lib = _lib()
+    rows = sorted({r for m in (0, 1, 8, 48) for r in range(max(m * E - 70, 0), m * E + 70)} | set(range(0, 20000, 61)))
+    never_shrinks(lambda r: lib.moe_expert_ffn_w8a8_workspace_size(r, H, E, I), rows)
+    k = min(8, E)
+    never_shrinks(lambda t: lib.moe_w8a8_workspace_size(t, H, E, k, I), range(0, 13000 // k))
