@@ -480,7 +480,9 @@ BalanceLayout balance_layout(int T, int E, int S) {
     if (L.per_block < kTokensPerBlockMin) L.per_block = kTokensPerBlockMin;
     if (T <= kOneBlockTokens) L.per_block = kOneBlockTokens;
     L.blocks = (T + L.per_block - 1) / L.per_block;
-    const size_t slots = static_cast<size_t>(L.blocks) + S;
+    // the blocks' upper bound, which grows with T as their number does not
+    const int finest = (T + kTokensPerBlockMin - 1) / kTokensPerBlockMin;
+    const size_t slots = static_cast<size_t>(finest < most ? finest : most) + S;
     L.ticket = 0;
     L.bounds = 256;
     L.seq_loss = L.bounds + align256((static_cast<size_t>(S) + 1) * 4);

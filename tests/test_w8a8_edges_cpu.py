@@ -26,3 +26,13 @@ def test_a_workspace_of_the_ffn_holds_fewer_rows_too(H, E, I):
     never_shrinks(lambda r: lib.moe_expert_ffn_w8a8_workspace_size(r, H, E, I), rows)
     k = min(8, E)
     never_shrinks(lambda t: lib.moe_w8a8_workspace_size(t, H, E, k, I), range(0, 13000 // k))
+
+
+@pytest.mark.parametrize("E,S", [(8, 1), (60, 3), (128, 1), (256, 65535)])
+def test_a_workspace_of_the_balance_loss_holds_fewer_tokens_too(E, S):
+    lib = _lib()
+    tokens = sorted(set(range(0, 20000, 7)) | set(range(9400, 9600)) | set(range(0, 6000000, 4999)) |
+                    {148 * 1024 * 32 * n + d for n in (1, 2, 3) for d in (-1, 0, 1)})
+    never_shrinks(lambda t: lib.moe_balance_loss_workspace_size(t, E, S), tokens)
+    never_shrinks(lambda s: lib.moe_balance_loss_workspace_size(5000, E, s), range(1, 3000))
+    never_shrinks(lambda e: lib.moe_balance_loss_workspace_size(1 << 24, e, S), range(1, 257))
