@@ -135,7 +135,7 @@ bool valid_w8a8_ffn(int H, int I) {
 // boundaries: a 128-byte slice of a row then lies in one line of the L2 cache, which the
 // loads of the products go by (rows of 704 bytes: two lines each).
 struct W8a8Layout {
-    size_t err, counters, clear_end, xq, xs, act, aq, as, total;
+    size_t err, counters, counters_end, xq, xs, act, aq, as, total;
     int ldx, lda;   // bytes a row of xq, aq
 };
 
@@ -145,7 +145,7 @@ W8a8Layout w8a8_layout(int rows, int H, int E, int I) {
     W8a8Layout L;
     L.err = c.take(kAlign);
     L.counters = c.take(static_cast<size_t>(q8_ffn_counters(rows, E)) * 4);
-    L.clear_end = q8_ffn_supported(rows, E, I) ? c.off : L.counters;
+    L.counters_end = c.off;
     L.ldx = (H + 127) / 128 * 128;
     L.lda = (I + 127) / 128 * 128;
     L.xq = c.take(r * L.ldx);
@@ -814,10 +814,11 @@ static moe_status w8a8_ffn(const void* x, const int32_t* perm_dst, int T, int k,
     q.perm_dst = perm_dst;
     q.k = k;
     q.rows_out = rows;
+    const bool one_launch = q8_ffn_supported(rows, E, I);
     q.clear = reinterpret_cast<int32_t*>(ws + L.err);
-    q.clear_words = static_cast<int>((L.clear_end - L.err) / 4);
+    q.clear_words = static_cast<int>(((one_launch ? L.counters_end : L.counters) - L.err) / 4);
     MOE_CUDA(launch_quantize_rows(q, s));
-    if (q8_ffn_supported(rows, E, I)) {
+    if (one_launch) {
         Q8FfnArgs f;
         f.x_q = xq;
         f.ldx = L.ldx;

@@ -473,6 +473,7 @@ int lanes_per_row(int E) {
 // kFold rows instead 97.)
 BalanceLayout balance_layout(int T, int E, int S) {
     BalanceLayout L;
+    // a fixed count: the same cut, so the same bits, on any GPU, and sizes that need no device
     const int sms = 148, range = kMostRows * kBWarps * (32 / lanes_per_row(E));
     const int each = (T + sms - 1) / sms;
     const int most = sms * (each > range ? (each + range - 1) / range : 1);

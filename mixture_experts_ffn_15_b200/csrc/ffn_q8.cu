@@ -539,7 +539,7 @@ q8_ffn_kernel(const __grid_constant__ CUtensorMap tmW1, const __grid_constant__ 
 }  // namespace
 
 // One launch for up to 48 rows per expert on average; with 8 rows and more, only where fc1 has
-// more than two rounds of units for the CTA pairs (E ceil(2I / 256) > 148), since the separate
+// more than two rounds of units for the CTA pairs (E ceil(2I / 256) > SMs), since the separate
 // kernels (row quantiser, fc1, row quantiser, fc2) then have no stream to lose between them
 // and shorter waits.  Measured (one launch / separate, us): E = 128, H = 2816, I = 704: 32
 // rows 41.8 / 54.3, 1024 rows 127.0 / 158.1, 48 rows per expert 180.7 / 186.1, 64 per expert
@@ -550,7 +550,7 @@ constexpr int kMostPerExpert = 48;
 
 bool q8_ffn_supported(int rows, int E, int I) {
     const long long r = rows;
-    return r <= static_cast<long long>(kMostPerExpert) * E && (r < 8LL * E || static_cast<long long>(E) * ((2 * I + 255) / 256) > 148);
+    return r <= static_cast<long long>(kMostPerExpert) * E && (r < 8LL * E || static_cast<long long>(E) * ((2 * I + 255) / 256) > device_sm_count());
 }
 
 // Two words per chunk and the scheduler's; for more rows than the kernel takes, those of the most.
