@@ -293,8 +293,10 @@ moe_status moe_matmul_q8(const int8_t* a_q, const float* a_scale, const int8_t* 
  *   fc1_layout, fc2_q [E, H, I] and fc2_scale [E, H]; fc1_bias [E, 2I], fc2_bias [E, H]
  *   bf16 or NULL; y_perm [rows, H] bf16, rows at or beyond offsets[E] not written
  *   workspace at least moe_expert_ffn_w8a8_workspace_size(rows, H, E, I) bytes, 256-byte
- *   aligned, any contents; its first word is the call's device error word.
- * H and I multiples of 32, at most 65536. */
+ *   aligned, any contents; its first word is the call's device error word, cleared at
+ *   the start of every call with rows.
+ * H and I multiples of 32, at most 65536.  rows = 0 is a no-op: nothing is enqueued and
+ * nothing written, the error word included. */
 size_t moe_expert_ffn_w8a8_workspace_size(int rows, int H, int E, int I);
 moe_status moe_expert_ffn_w8a8(const void* x_perm, const int32_t* offsets, const int8_t* fc1_q,
                                const float* fc1_scale, const int8_t* fc2_q, const float* fc2_scale,
@@ -304,8 +306,9 @@ moe_status moe_expert_ffn_w8a8(const void* x_perm, const int32_t* offsets, const
 
 /* The whole layer on moe_expert_ffn_w8a8: [pre-FFN RMSNorm ->] route (on the bf16 input)
  * -> permute -> int8 expert FFN -> combine.  Arguments as moe_forward_q8; any batch size.
- * workspace >= moe_w8a8_workspace_size(T, H, E, k, I) bytes, 256-byte aligned; its first
- * word is the device error word. */
+ * workspace >= moe_w8a8_workspace_size(T, H, E, k, I) bytes, 256-byte aligned, any contents;
+ * its first word is the device error word, cleared at the start of every call with tokens.
+ * T = 0 is a no-op: nothing is enqueued and nothing written, the error word included. */
 size_t moe_w8a8_workspace_size(int T, int H, int E, int k, int I);
 moe_status moe_forward_w8a8(const void* hidden, const void* norm_weight, float norm_eps,
                             const void* router_w, const float* router_bias, const int8_t* fc1_q,

@@ -282,7 +282,7 @@ def expert_ffn_w8a8(x_perm, offsets, fc1_q, fc1_scale, fc2_q, fc2_scale, y_perm=
     """expert_ffn with int8 weights and int8 activations (quantize_rows before either
     product), for any number of rows per expert; weights and scales as in forward_q8.
     Rows at or beyond offsets[E] are not written (zeros when y_perm is not given).  The
-    workspace's first word is the call's error word (get_error)."""
+    workspace's first word is the call's error word (get_error), zero after an empty call too."""
     _need(x_perm, "x_perm", torch.bfloat16)
     rows, H = x_perm.shape
     E, two_i, _ = fc1_q.shape
@@ -302,6 +302,8 @@ def expert_ffn_w8a8(x_perm, offsets, fc1_q, fc1_scale, fc2_q, fc2_scale, y_perm=
         _need(workspace, "workspace", torch.uint8)
         _same_device(x_perm, offsets, fc1_q, fc1_scale, fc2_q, fc2_scale, fc1_bias, fc2_bias,
                      y_perm, workspace)
+        if rows == 0:   # the C call is a no-op then
+            workspace[:4].zero_()
         check(_lib().moe_expert_ffn_w8a8(_addr(x_perm), _addr(offsets), _addr(fc1_q), _addr(fc1_scale),
                                          _addr(fc2_q), _addr(fc2_scale), _addr(fc1_bias),
                                          _addr(fc2_bias), rows, H, E, I, _swiglu(*swiglu),
@@ -320,7 +322,8 @@ def forward_w8a8(hidden, router_w, fc1_q, fc1_scale, fc2_q, fc2_scale, k, normal
                  swiglu=(1.0, 0.0, float("inf")), fc1_bias=None, fc2_bias=None,
                  fc1_layout="interleaved", norm_weight=None, norm_eps=1e-6):
     """The layer with int8 experts and int8 activations in the expert products (the router
-    reads the bf16 input): arguments as forward_q8, any batch size."""
+    reads the bf16 input): arguments as forward_q8, any batch size.  The workspace's first
+    word is the call's error word (get_error), zero after an empty call too."""
     _need(hidden, "hidden", torch.bfloat16)
     T, H = hidden.shape
     E = router_w.shape[0]
@@ -344,6 +347,8 @@ def forward_w8a8(hidden, router_w, fc1_q, fc1_scale, fc2_q, fc2_scale, k, normal
         _need(workspace, "workspace", torch.uint8)
         _same_device(hidden, router_w, router_bias, fc1_q, fc1_scale, fc2_q, fc2_scale, fc1_bias,
                      fc2_bias, norm_weight, out, workspace)
+        if T == 0:   # the C call is a no-op then
+            workspace[:4].zero_()
         check(_lib().moe_forward_w8a8(_addr(hidden), _addr(norm_weight), float(norm_eps),
                                       _addr(router_w), _addr(router_bias), _addr(fc1_q),
                                       _addr(fc1_scale), _addr(fc2_q), _addr(fc2_scale), _addr(fc1_bias),

@@ -6,6 +6,7 @@ import pytest
 import torch
 
 import mixture_experts_ffn_15_b200 as moe
+from mixture_experts_ffn_15_b200 import _abi
 from test_gpu_w8a8 import OSS, STD, _ffn_case, dev
 
 pytestmark = pytest.mark.gpu
@@ -75,3 +76,22 @@ def test_quantize_rows_of_more_than_2_31_threads():
         assert torch.equal(s[a:a + step], top[:, 0].float() / torch.full_like(s[a:a + step], 127))
         # 127 v is exact in float64, the quotient is a half exactly or far from one
         assert torch.equal(q[a:a + step], (127 * v / top.clamp_min(1e-300)).round().to(torch.int8))
+
+
+@pytest.mark.parametrize("stream", [False, True])
+def test_the_error_word_of_an_empty_call_is_zero(stream):
+    """A workspace may hold anything; so may the last call's error."""
+    _, _, _, q1, s1, q2, s2, _, _ = _ffn_case(8, 64, 32, 4, None, False, 34)
+    w = [dev(a) for a in (q1, s1, q2, s2)]
+    x = torch.zeros((0, 64), dtype=torch.bfloat16, device="cuda")
+    router = torch.zeros((4, 64), dtype=torch.bfloat16, device="cuda")
+    off = torch.zeros(5, dtype=torch.int32, device="cuda")
+    for n, call in ((moe.expert_ffn_w8a8_workspace_size(0, 64, 4, 32), lambda **kw: moe.expert_ffn_w8a8(x, off, *w, **kw)),
+                    (moe.w8a8_workspace_size(0, 64, 4, 2, 32), lambda **kw: moe.forward_w8a8(x, router, *w, 2, **kw))):
+        ws = torch.full((n,), 0xA5, dtype=torch.uint8, device="cuda")
+        torch.cuda.synchronize()
+        st = torch.cuda.Stream() if stream else None
+        y = call(workspace=ws, stream=st)
+        torch.cuda.synchronize()
+        assert y.shape == (0, 64) and moe.get_error(moe.workspace_error_word(ws)) == (_abi.MOE_OK, 0)
+        assert torch.all(ws[4:] == 0xA5)
