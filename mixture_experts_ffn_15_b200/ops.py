@@ -197,7 +197,10 @@ def _addr(t):
 
 
 _HERE = contextlib.nullcontext()
-_raw_stream = torch._C._cuda_getCurrentRawStream   # of a device: 0.1 us, a Stream object 3 us
+# The current stream's handle of a device: 0.1 us, a Stream object 3 us.  (A torch build without
+# CUDA lacks the function; the package imports there, for the C library and the checks.)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda i: torch.cuda.current_stream(i).cuda_stream)
 
 
 def _on(t, stream):

@@ -1,6 +1,11 @@
-"""int8 products and balance loss without a GPU: workspace sizes over whole ranges, refusals."""
+"""int8 products and balance loss without a GPU: workspace sizes over whole ranges, the
+binding on a torch build without CUDA."""
+import subprocess
+import sys
+
 import pytest
 
+from conftest import ROOT
 from mixture_experts_ffn_15_b200 import _abi
 from mixture_experts_ffn_15_b200.build import build
 
@@ -36,3 +41,15 @@ def test_a_workspace_of_the_balance_loss_holds_fewer_tokens_too(E, S):
     never_shrinks(lambda t: lib.moe_balance_loss_workspace_size(t, E, S), tokens)
     never_shrinks(lambda s: lib.moe_balance_loss_workspace_size(5000, E, s), range(1, 3000))
     never_shrinks(lambda e: lib.moe_balance_loss_workspace_size(1 << 24, e, S), range(1, 257))
+
+
+def test_the_package_imports_on_a_torch_build_without_cuda():
+    """Such a build has no _cuda_getCurrentRawStream; the argument checks work all the same."""
+    code = ("import torch\n"
+            "if hasattr(torch._C, '_cuda_getCurrentRawStream'): del torch._C._cuda_getCurrentRawStream\n"
+            "import mixture_experts_ffn_15_b200 as moe\n"
+            "try: moe.quantize_rows(torch.zeros(2, 8))\n"
+            "except ValueError as e: assert 'CUDA' in str(e)\n"
+            "else: raise SystemExit('not refused')\n")
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr
