@@ -277,7 +277,8 @@ moe_status moe_quantize_rows(const void* x, int rows, int K, moe_dtype dt, int8_
  *   err_word int32 device word or NULL: MOE_DEVERR_BAD_EXPERT is OR-ed in for offsets that
  *            decrease or leave [0, rows] (they are clamped), MOE_DEVERR_TIMEOUT for a
  *            bounded wait that ran out; never cleared here
- * K a multiple of 16 and at most 65536, N a multiple of 32.  rows = 0 is a no-op. */
+ * K a multiple of 16 and at most 65536, N a multiple of 32 and at most 2^30.  The two
+ * scales are multiplied with each other first, in float32.  rows = 0 is a no-op. */
 moe_status moe_matmul_q8(const int8_t* a_q, const float* a_scale, const int8_t* w_q,
                          const float* w_scale, const void* bias, const int32_t* offsets, int rows,
                          int K, int E, int N, moe_dtype out_dt, void* out, int32_t* err_word,
@@ -339,7 +340,8 @@ moe_status moe_forward_w8a8(const void* hidden, const void* norm_weight, float n
  *               any contents
  * A logit of -infinity has probability 0; a token whose logits are all -infinity has no
  * probabilities (0 each) and no gradient, but still counts.  NaN and +infinity propagate.
- * The results do not depend on the order of anything: the same bits on every call. */
+ * The results do not depend on the order of anything: the same bits on every call.
+ * T k and T at most 2^30, S at most 65535, k at most E. */
 size_t moe_balance_loss_workspace_size(int T, int E, int S);
 moe_status moe_balance_loss(const float* logits, const int32_t* topk_idx, const uint8_t* mask,
                             const int32_t* seq_offsets, int T, int E, int k, int S, float coef,

@@ -122,7 +122,7 @@ PermLayout perm_layout(int T, int E) {
 constexpr int kQ8MaxK = 65536;
 constexpr int kMaxSequences = 65535;   // of the balance loss: one block each
 bool valid_q8_k(int K) { return K > 0 && K % 16 == 0 && K <= kQ8MaxK; }
-bool valid_q8_n(int N) { return N > 0 && N % 32 == 0; }
+bool valid_q8_n(int N) { return N > 0 && N % 32 == 0 && N <= (1 << 30); }
 bool valid_q8_rows(int rows) { return rows >= 0 && rows <= (1 << 30); }
 bool valid_w8a8_ffn(int H, int I) {
     return H > 0 && I > 0 && H % 32 == 0 && I % 32 == 0 && H <= kQ8MaxK && I <= kQ8MaxK;
@@ -974,7 +974,7 @@ moe_status moe_forward_w8a8(const void* hidden, const void* norm_weight, float n
 }
 
 size_t moe_balance_loss_workspace_size(int T, int E, int S) {
-    if (T < 0 || E <= 0 || E > kMaxExperts || S < 1 || S > kMaxSequences) return 0;
+    if (T < 0 || T > (1 << 30) || E <= 0 || E > kMaxExperts || S < 1 || S > kMaxSequences) return 0;
     return balance_workspace_bytes(T, E, S);
 }
 

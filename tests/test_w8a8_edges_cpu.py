@@ -1,5 +1,6 @@
 """int8 products and balance loss without a GPU: workspace sizes over whole ranges, the
 binding on a torch build without CUDA."""
+import ctypes
 import subprocess
 import sys
 
@@ -53,3 +54,14 @@ def test_the_package_imports_on_a_torch_build_without_cuda():
             "else: raise SystemExit('not refused')\n")
     r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, r.stderr
+
+
+def test_sizes_whose_tiles_would_pass_32_bits_are_refused():
+    lib, P = _lib(), ctypes.c_void_p(4096)
+    inv = _abi.MOE_ERR_INVALID_ARG
+    for n in ((1 << 30) + 32, (1 << 31) - 32):
+        assert lib.moe_matmul_q8(P, P, P, P, None, None, 4, 16, 1, n, 1, P, None, None) == inv
+        assert lib.moe_matmul_q8(P, P, P, P, None, P, 4000, 16, 2, n, 1, P, None, None) == inv
+    for t in ((1 << 30) + 1, (1 << 31) - 1):
+        assert lib.moe_balance_loss_workspace_size(t, 8, 1) == 0
+    assert lib.moe_balance_loss_workspace_size(1 << 30, 8, 1) > 0
