@@ -113,6 +113,16 @@ __device__ __forceinline__ bool wait_count(const int32_t* ctr, int target, volat
     }
 }
 
+// The same for a whole warp, whose lanes then read what the counter stands for: the shuffle
+// alone orders no memory, the barrier behind it does.
+__device__ __forceinline__ bool wait_count_warp(const int32_t* ctr, int target, volatile int* abort, int lane) {
+    bool ok = true;
+    if (lane == 0) ok = wait_count(ctr, target, abort);
+    ok = __shfl_sync(0xffffffffu, ok, 0);
+    __syncwarp();
+    return ok;
+}
+
 __device__ __forceinline__ void fence_proxy_async_global() { asm volatile("fence.proxy.async.global;" ::: "memory"); }
 
 // The int8 rows of activation rows row and row + 1 (if `two`), by one warp.
@@ -420,11 +430,7 @@ q8_ffn_kernel(const __grid_constant__ CUtensorMap tmW1, const __grid_constant__ 
                     if (b) bias[i] = bf16_at(b, j);
                 }
             }
-            if (!f1) {
-                bool ok = true;
-                if (lane == 0) ok = wait_count(p.ready + d.chunk, d.nrows, abort_flag);
-                if (!__shfl_sync(0xffffffffu, ok, 0)) break;
-            }
+            if (!f1 && !wait_count_warp(p.ready + d.chunk, d.nrows, abort_flag, lane)) break;
             Scales& sc = s_scales[at];
 #pragma unroll
             for (int i = 0; i < kTok / 32; ++i)
@@ -453,9 +459,7 @@ q8_ffn_kernel(const __grid_constant__ CUtensorMap tmW1, const __grid_constant__ 
             const int row0 = s_off[g] + (chunk - s_pre[g]) * kTok;
             const int n = min(2, min(kTok, s_off[g + 1] - row0) - r0);
             if (n <= 0) continue;
-            bool ok = true;
-            if (lane == 0) ok = wait_count(p.done + chunk, 4 * MT1, abort_flag);
-            if (!__shfl_sync(0xffffffffu, ok, 0)) break;
+            if (!wait_count_warp(p.done + chunk, 4 * MT1, abort_flag, lane)) break;
             round_rows(p, row0 + r0, n == 2, lane);
             fence_proxy_async_global();   // read by TMA
             __threadfence();
