@@ -99,3 +99,57 @@ def test_long_ranges(E):
         assert torch.equal(r["counts"][s].long(), torch.bincount(idx[a:z, 0][m], minlength=E))
         want = p[a:z][m].sum(0) / max(n, 1)
         assert torch.all((r["probs"][s].double() - want).abs() <= 128 * 2.0 ** -24 * want)
+
+
+def reference(lg, idx, k, coef, mask, seq):
+    """loss, counts, probs, dlogits and the gradient's bound in float64, whole tensors at a time."""
+    T, E = lg.shape
+    p = torch.softmax(lg.double(), 1)
+    bounds = torch.tensor([0, T] if seq is None else list(seq), device="cuda")
+    S = bounds.numel() - 1
+    sid = torch.searchsorted(bounds[1:].contiguous(), torch.arange(T, device="cuda"), right=True).clamp_max(S - 1)
+    live = (torch.arange(T, device="cuda") < bounds[-1]) & (torch.ones(T, dtype=torch.bool, device="cuda") if mask is None else mask)
+    n = torch.zeros(S, dtype=torch.long, device="cuda").index_add_(0, sid, live.long())
+    flat = (sid[:, None] * E + idx.long())[live].reshape(-1)
+    counts = torch.bincount(flat, minlength=S * E).view(S, E)
+    probs = torch.zeros((S, E), dtype=torch.float64, device="cuda").index_add_(0, sid, p * live[:, None])
+    nd = n.clamp_min(1).double()
+    probs = probs / nd[:, None]
+    f = counts / (nd[:, None] * k)
+    f0 = torch.where(n[:, None] > 0, f - 1.0 / E, 0.0)[sid]
+    dot, mag = (p * f0).sum(1, keepdim=True), (p * f0.abs()).sum(1, keepdim=True)
+    scale = (coef * E / (S * nd))[sid][:, None] * live[:, None]
+    # the bound of test_gpu_balance, the reference's own rounding from f - 1/E instead of f
+    own = (E + 4) * 2.0 ** -53 * f.amax(1)[sid][:, None]
+    bound = scale * p * (160 * 2.0 ** -24 * ((f0 - dot).abs() + mag) + own) + 1e-37
+    return coef / S * E * (f * probs).sum(), counts, probs, n, scale * p * (f0 - dot), bound
+
+
+@pytest.mark.parametrize("E", [256, 255, 128, 97, 12])
+@pytest.mark.parametrize("S", [0, 1, 20, 700])
+@pytest.mark.parametrize("masked", [False, True])
+def test_blocks_of_many_rows(E, S, masked):
+    """Up to 13 rows a lane forward and 17 backward, two of them loaded ahead, with sequence
+    bounds inside the blocks and a tail that belongs to no sequence."""
+    T, k = 60013, min(8, E)
+    g = torch.Generator(device="cuda").manual_seed(E + S)
+    lg = torch.randn((T, E), generator=g, device="cuda") * 1.5 + torch.randn(E, generator=g, device="cuda")
+    idx = torch.topk(lg, k, 1).indices.int()
+    mask = torch.rand(T, generator=g, device="cuda") < 0.7 if masked else None
+    seq = None
+    if S:
+        rng = np.random.default_rng(S)
+        seq = np.concatenate([[0], np.sort(rng.integers(0, T + 1, S - 1)), [T - 11]])
+        seq = np.minimum(seq, T - 11)
+    s = None if seq is None else torch.from_numpy(seq.astype(np.int32)).cuda()
+    r = moe.balance_loss(lg, idx, coef=0.01, mask=mask, seq_offsets=s)
+    d = moe.balance_loss_backward(lg, k, r["counts"], r["tokens"], coef=0.01, mask=mask, seq_offsets=s)
+    loss, counts, probs, n, grad, bound = reference(lg, idx, k, 0.01, mask, seq)
+    assert torch.equal(r["counts"].long(), counts) and torch.equal(r["tokens"].long(), n)
+    U32 = 2.0 ** -24
+    assert torch.all((r["probs"].double() - probs).abs() <= 128 * U32 * probs + 1e-37)
+    assert abs(float(r["loss"]) - float(loss)) <= 132 * U32 * float(loss)
+    over = (d.double() - grad).abs() - bound
+    assert torch.all(over <= 0), (float(over.max()), int(over.argmax()) // E)
+    again = moe.balance_loss(lg, idx, coef=0.01, mask=mask, seq_offsets=s)
+    assert all(torch.equal(again[a], r[a]) for a in r)

@@ -7,7 +7,9 @@ import torch
 
 import mixture_experts_ffn_15_b200 as moe
 from mixture_experts_ffn_15_b200 import _abi
-from test_gpu_w8a8 import OSS, STD, _ffn_case, dev
+from parity_util import from_dev
+from test_gpu_w8a8 import OSS, STD, _dev_bias, _ffn_case, _ffn_ref, dev
+from w8a8_util import check
 
 pytestmark = pytest.mark.gpu
 
@@ -95,3 +97,61 @@ def test_the_error_word_of_an_empty_call_is_zero(stream):
         torch.cuda.synchronize()
         assert y.shape == (0, 64) and moe.get_error(moe.workspace_error_word(ws)) == (_abi.MOE_OK, 0)
         assert torch.all(ws[4:] == 0xA5)
+
+
+# The one launch's rounding holds 1024 values of a row in registers and reads the rest again.
+LONG = [  # rows, H, I, E, used, layout, act, biases
+    (20, 64, 1056, 4, None, "interleaved", STD, False),
+    (9, 96, 2080, 2, None, "chunked", OSS, True),
+    (500, 64, 1216, 80, 5, "chunked", STD, True),          # several chunks an expert, odd ends
+    (3, 32, 4128, 1, None, "interleaved", OSS, False),
+    (7, 128, 1024, 1, None, "interleaved", STD, False),
+    (33, 160, 992, 5, 2, "chunked", OSS, False),
+]
+
+
+@pytest.mark.parametrize("rows,H,I,E,used,layout,act,biases", LONG)
+def test_one_launch_with_long_activation_rows(rows, H, I, E, used, layout, act, biases):
+    x, xv, off, q1, s1, q2, s2, b1, b2 = _ffn_case(rows, H, I, E, used, biases, rows + I)
+    y = moe.expert_ffn_w8a8(x, dev(off), dev(q1), dev(s1), dev(q2), dev(s2), swiglu=act, fc1_layout=layout,
+                            fc1_bias=_dev_bias(b1), fc2_bias=_dev_bias(b2))
+    ref, bound = _ffn_ref(xv, off, q1, s1, q2, s2, b1[1], b2[1], layout, act)
+    check(from_dev(y), ref, bound, f"ffn {rows}x{H}x{I} E={E}")
+
+
+@pytest.mark.parametrize("at", [5, 1023, 1024, 1500, 2079])
+def test_one_launch_with_the_largest_activation_anywhere_in_its_row(at):
+    """One channel's scale raised 64-fold: its activations are the rows' largest."""
+    rows, H, I, E = 9, 96, 2080, 2
+    x, xv, off, q1, s1, q2, s2, _, _ = _ffn_case(rows, H, I, E, None, False, 35)
+    s1[:, 2 * at + 1] *= 64          # interleaved: the channel's up row
+    y = moe.expert_ffn_w8a8(x, dev(off), dev(q1), dev(s1), dev(q2), dev(s2))
+    ref, bound = _ffn_ref(xv, off, q1, s1, q2, s2, None, None, "interleaved", STD)
+    check(from_dev(y), ref, bound, f"largest at {at}")
+
+
+@pytest.mark.parametrize("T,E,k,layout", [(1, 16, 4, "interleaved"), (6, 64, 8, "chunked"), (90, 8, 2, "interleaved"),
+                                          (700, 8, 2, "chunked"), (900, 60, 4, "interleaved")])
+@pytest.mark.parametrize("norm", [False, True])
+def test_the_layer_with_biases_and_a_clipped_activation_equals_its_steps(T, E, k, layout, norm):
+    """forward_w8a8 with every option against rmsnorm, route, permute, expert_ffn_w8a8 and
+    combine.  The layer and moe_route may take different routers (float32 sums in another order):
+    weights within 1e-5, an output within that of the experts' magnitudes."""
+    H, I = 256, 96
+    rng = np.random.default_rng(T)
+    x, _, _, q1, s1, q2, s2, b1, b2 = _ffn_case(T, H, I, E, None, True, 36)
+    w = [dev(a) for a in (q1, s1, q2, s2)]
+    router = torch.from_numpy(rng.standard_normal((E, H)) / 16).bfloat16().cuda()
+    rb = torch.from_numpy((rng.standard_normal(E) * 0.3).astype(np.float32)).cuda()
+    nw = torch.from_numpy(rng.uniform(0.5, 1.5, H)).bfloat16().cuda() if norm else None
+    ffn = dict(swiglu=OSS, fc1_layout=layout, fc1_bias=b1[0].cuda(), fc2_bias=b2[0].cuda())
+    out = moe.forward_w8a8(x, router, *w, k, router_bias=rb, norm_weight=nw, **ffn)
+    xn = moe.rmsnorm(x, nw) if norm else x
+    r = moe.route(xn, router, k, router_bias=rb)
+    p = moe.permute(r["idx"], E, hidden=xn)
+    y = moe.expert_ffn_w8a8(p["x_perm"], p["offsets"], *w, **ffn)
+    want = moe.combine(y, p["perm_dst"], r["w"], T, k)
+    sure = r["near_tie"] == 0
+    d = (out.double() - want.double()).abs()
+    assert torch.all(d[sure] <= 1e-5 * k * float(y.float().abs().max()) + 2.0 ** -7 * want[sure].double().abs())
+    assert int(sure.sum()) > 0
