@@ -289,7 +289,9 @@ moe_status moe_matmul_q8(const int8_t* a_q, const float* a_scale, const int8_t* 
  *   x_perm rows to int8 -> product with fc1_q -> SwiGLU in float32 -> activation rows to
  *   int8 -> product with fc2_q -> y_perm in bf16
  * each step as in moe_quantize_rows and moe_matmul_q8; the activations are not rounded
- * between the SwiGLU and their int8.
+ * between the SwiGLU and their int8.  The SwiGLU's sigmoid uses the fast exponential and
+ * quotient: an activation is within (16 + 3 |alpha gate|) 2^-24 of itself for its gate and
+ * up values.  A row of x_perm that holds an infinity or a NaN gives a row of NaN.
  *   x_perm [rows, H] bf16, offsets [E+1]; fc1_q [E, 2I, H] int8 and fc1_scale [E, 2I] in
  *   fc1_layout, fc2_q [E, H, I] and fc2_scale [E, H]; fc1_bias [E, 2I], fc2_bias [E, H]
  *   bf16 or NULL; y_perm [rows, H] bf16, rows at or beyond offsets[E] not written
@@ -338,6 +340,9 @@ moe_status moe_forward_w8a8(const void* hidden, const void* norm_weight, float n
  *               (clamped to [0, T]; one below an earlier one counts as that one)
  *   workspace   at least moe_balance_loss_workspace_size(T, E, S) bytes, 256-byte aligned,
  *               any contents
+ * The softmax uses the fast exponential: a probability is within (18 + 2.3 |logit - row's
+ * largest|) 2^-24 of itself, and their sums add at most 100 roundings of 2^-24 before they
+ * go on in float64.
  * A logit of -infinity has probability 0; a token whose logits are all -infinity has no
  * probabilities (0 each) and no gradient, but still counts.  NaN and +infinity propagate.
  * The results do not depend on the order of anything: the same bits on every call.

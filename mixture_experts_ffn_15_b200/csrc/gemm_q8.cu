@@ -342,7 +342,8 @@ q8_stream_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
 // at N = 256 where its four MMAs take 512: an SM takes in about 50 bytes a cycle from L2.
 // Barriers a slot instead of two slots: 745 cycles.  Weight tiles kept in shared memory for
 // several token tiles change nothing at K = 704 (171.5 us against 175.5, 176.6 against
-// 175.9), where the stores of the outputs bound the unit.  Measured: 8191 rows, 4096 -> 4096,
+// 175.9): of the ~5400 cycles a unit takes there, intake accounts for 3900, beside the
+// epilogue's 2200; which wait holds the rest has not been measured.  Measured: 8191 rows, 4096 -> 4096,
 // 95 us (2896 TOP/s); E = 128, 65536 rows: 2816 -> 2 x 704 with SwiGLU 284 us, 704 -> 2816
 // 178 us (369 MB of outputs), the clock held to ~1.45 GHz by the power cap.
 constexpr int kPEpi = 16;
