@@ -157,7 +157,9 @@ gather_by_token_kernel(const uint4* __restrict__ hidden, const int32_t* __restri
         const uint4* s = hidden + static_cast<size_t>(t) * vec_per_row;
         const int v_end = min(vec_per_row, (c + 1) * chunk_vecs);
         // 8 loads in flight per lane before the stores
-        for (int v0 = c * chunk_vecs + lane; v0 < v_end; v0 += 32 * 8) {
+        // (the whole warp stays in the loop: lanes past the row's end hold rows to hand out)
+        for (int base = c * chunk_vecs; base < v_end; base += 32 * 8) {
+            const int v0 = base + lane;
             uint4 buf[8];
 #pragma unroll
             for (int q = 0; q < 8; ++q)
