@@ -113,7 +113,9 @@ int32_t* moe_workspace_error_word(void* workspace);
  *   logits      [T, E] float32 out (required): the logits the selection was made on
  *   near_tie    [T] int32 out or NULL: bit 1 = the k-th and (k+1)-th logits differ by
  *               less than 1e-5, bit 2 = two adjacent chosen logits do
- * T = 0 is a no-op. */
+ * A token with fewer than k logits above -infinity (experts masked by a bias of -infinity)
+ * takes the lowest of the others, with weight 0; one whose logits are all NaN keeps k valid
+ * experts, with weights NaN.  T = 0 is a no-op. */
 moe_status moe_route(const void* hidden, const void* router_w, const float* router_bias,
                      int T, int H, int E, int k, int normalize, moe_dtype dt,
                      int32_t* topk_idx, float* topk_w, float* logits, int32_t* near_tie,

@@ -142,6 +142,16 @@ __global__ void __launch_bounds__(kHistThreads) topk_hist_kernel(const TopkHistA
                         bi = oi;
                     }
                 }
+                if (bi >= E) {
+                    // only NaN left: the lowest of those experts, so that ids stay valid and the
+                    // token's weights become NaN
+                    int low = 0x7fffffff;
+#pragma unroll
+                    for (int i = kLanesVals - 1; i >= 0; --i)
+                        if (lane + 32 * i < E && !((taken >> i) & 1u)) low = lane + 32 * i;
+                    bi = __reduce_min_sync(0xffffffffu, low);
+                    bv = __uint_as_float(0x7fc00000u);
+                }
                 if (bi < E && (bi & 31) == lane) taken |= 1u << (bi >> 5);
                 if (lane == 0) {
                     s_val[warp][r] = bv;

@@ -25,6 +25,33 @@ namespace {
 using namespace sm100;
 using namespace tc;
 
+// The insertions below take logits above -infinity only.  Where fewer than k are (experts
+// masked by a bias of -infinity, a token that is not finite), the empty slots at the list's end
+// take the lowest experts that are not in it: -infinity ties go to the lower index, and a row
+// of NaN keeps valid ids and weights of NaN.
+template <int KS>
+__device__ __forceinline__ void fill_empty(int (&ids)[KS], int k) {
+    int missing = 0;
+#pragma unroll
+    for (int j = 0; j < KS; ++j) missing += j < k && ids[j] < 0;
+#pragma unroll 1
+    for (int e = 0; missing > 0; ++e) {
+        bool in_list = false;
+#pragma unroll
+        for (int j = 0; j < KS; ++j) in_list = in_list || ids[j] == e;
+        if (in_list) continue;
+        bool placed = false;
+#pragma unroll
+        for (int j = 0; j < KS; ++j) {
+            if (!placed && ids[j] < 0) {
+                ids[j] = e;
+                placed = true;
+            }
+        }
+        --missing;
+    }
+}
+
 // Routing of one 128-token tile from its logits in TMEM (columns 0..E-1, thread =
 // token row).  Each thread keeps the KS = k+1 (or more) largest biased logits in a
 // register list sorted descending, inserting the experts in index order so that equal
@@ -78,7 +105,8 @@ __device__ __forceinline__ void route_epilogue(uint32_t tb, bool valid, size_t r
             }
         }
     }
-    // rows past the batch hold bias-only logits (their A rows were zero-filled): finite
+    fill_empty<KS>(ids, k);
+    // rows past the batch hold bias-only logits (their A rows were zero-filled)
     const float vmax = vals[0];
     float den = 0.f;
     if (rp.normalize) {
@@ -353,6 +381,7 @@ __device__ __forceinline__ void route_row(const float* logit, const float* s_bia
             }
         }
     }
+    fill_empty<KS>(ids, k);
     const float vmax = vals[0];
     float den = 0.f;
     if (rp.normalize) {
