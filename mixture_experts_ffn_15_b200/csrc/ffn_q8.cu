@@ -92,39 +92,6 @@ struct __align__(16) Unit {
 };
 enum Kind : int { kNone = -1, kFc2 = 0, kFc1 = 1 };
 
-__device__ __forceinline__ int ld_acquire(const int32_t* p) {
-    int v;
-    asm volatile("ld.acquire.gpu.global.b32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
-    return v;
-}
-
-// Bounded wait for *ctr >= target, by one lane.
-__device__ __forceinline__ bool wait_count(const int32_t* ctr, int target, volatile int* abort) {
-    if (ld_acquire(ctr) >= target) return true;
-    const uint64_t t0 = global_timer_ns();
-    for (;;) {
-        __nanosleep(64);
-        if (ld_acquire(ctr) >= target) return true;
-        if (*abort) return false;
-        if (global_timer_ns() - t0 > kWaitNs) {
-            *abort = 1;
-            return false;
-        }
-    }
-}
-
-// The same for a whole warp, whose lanes then read what the counter stands for: the shuffle
-// alone orders no memory, the barrier behind it does.
-__device__ __forceinline__ bool wait_count_warp(const int32_t* ctr, int target, volatile int* abort, int lane) {
-    bool ok = true;
-    if (lane == 0) ok = wait_count(ctr, target, abort);
-    ok = __shfl_sync(0xffffffffu, ok, 0);
-    __syncwarp();
-    return ok;
-}
-
-__device__ __forceinline__ void fence_proxy_async_global() { asm volatile("fence.proxy.async.global;" ::: "memory"); }
-
 // The int8 rows of activation rows row and row + 1 (if `two`), by one warp.
 __device__ __forceinline__ void round_rows(const Params& p, int row, bool two, int lane) {
     const int nvec = p.I / 4, ldw = p.lda / 4;
@@ -343,7 +310,7 @@ q8_ffn_kernel(const __grid_constant__ CUtensorMap tmW1, const __grid_constant__ 
                 const CUtensorMap* mx = d.kind == kFc1 ? &tmX : &tmA;
                 const int nk = d.kind == kFc1 ? nk1 : nk2;
                 if (d.kind == kFc2) {
-                    if (!wait_count(p.ready + d.chunk, d.nrows, abort_flag)) break;
+                    if (!wait_count(p.ready + d.chunk, d.nrows, abort_flag, kWaitNs)) break;
                     fence_proxy_async_global();
                 }
                 const int nl = (d.nrows + kBox - 1) / kBox;
@@ -430,7 +397,7 @@ q8_ffn_kernel(const __grid_constant__ CUtensorMap tmW1, const __grid_constant__ 
                     if (b) bias[i] = bf16_at(b, j);
                 }
             }
-            if (!f1 && !wait_count_warp(p.ready + d.chunk, d.nrows, abort_flag, lane)) break;
+            if (!f1 && !wait_count_warp(p.ready + d.chunk, d.nrows, abort_flag, kWaitNs, lane)) break;
             Scales& sc = s_scales[at];
 #pragma unroll
             for (int i = 0; i < kTok / 32; ++i)
@@ -459,7 +426,7 @@ q8_ffn_kernel(const __grid_constant__ CUtensorMap tmW1, const __grid_constant__ 
             const int row0 = s_off[g] + (chunk - s_pre[g]) * kTok;
             const int n = min(2, min(kTok, s_off[g + 1] - row0) - r0);
             if (n <= 0) continue;
-            if (!wait_count_warp(p.done + chunk, 4 * MT1, abort_flag, lane)) break;
+            if (!wait_count_warp(p.done + chunk, 4 * MT1, abort_flag, kWaitNs, lane)) break;
             round_rows(p, row0 + r0, n == 2, lane);
             fence_proxy_async_global();   // read by TMA
             __threadfence();

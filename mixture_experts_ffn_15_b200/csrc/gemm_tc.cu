@@ -145,16 +145,6 @@ constexpr int kRouteSmemBytes =
     kMaxExperts * (kFusedRouteMaxT / 32) * 4 +    // token masks per expert
     16 * 8 * 4;                                   // partial dot products (<= 16 warps)
 
-__device__ __forceinline__ int ld_acquire(const int32_t* p) {
-    int v;
-    asm volatile("ld.acquire.gpu.global.b32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
-    return v;
-}
-
-__device__ __forceinline__ void fence_proxy_async_global() {
-    asm volatile("fence.proxy.async.global;" ::: "memory");
-}
-
 // Two int8 weights held as float32 bit patterns 0x4B000000 | (b ^ 0x80) = 2^23 + 128 + b:
 // subtract 2^23 + 128 from both with one packed add.rn.f32x2 (exact, the differences are
 // the integers b) and pack the two upper halves -- b in bf16, exact for |b| <= 128 -- into
@@ -167,21 +157,6 @@ __device__ __forceinline__ uint32_t sub_magic_f32x2(uint32_t a, uint32_t b) {
         : "=l"(d)
         : "r"(a), "r"(b), "l"(0xCB000080CB000080ull));   // -(2^23 + 128) in both halves
     return __byte_perm(static_cast<uint32_t>(d), static_cast<uint32_t>(d >> 32), 0x7632u);
-}
-
-__device__ __forceinline__ bool wait_count(const int32_t* ctr, int target, volatile int* abort,
-                                           uint64_t limit_ns = kWaitLimitNs) {
-    if (ld_acquire(ctr) >= target) return true;
-    const uint64_t t0 = global_timer_ns();
-    for (;;) {
-        __nanosleep(64);
-        if (ld_acquire(ctr) >= target) return true;
-        if (*abort) return false;
-        if (global_timer_ns() - t0 > limit_ns) {
-            *abort = 1;
-            return false;
-        }
-    }
 }
 
 struct DUnit {
@@ -538,9 +513,7 @@ tc_ffn_decode_kernel(const __grid_constant__ CUtensorMap tmW1, const __grid_cons
                 bbytes = static_cast<uint32_t>(nl4 * 4 * BK * 2);
             }
             if (!f1) {
-                bool ok = true;
-                if (lane == 0) ok = wait_count(&p.done[d.chunk], fc1_done, abort_flag);
-                if (!__shfl_sync(0xffffffffu, ok, 0)) break;
+                if (!wait_count_warp(&p.done[d.chunk], fc1_done, abort_flag, kWaitLimitNs, lane)) break;
                 fence_proxy_async_global();
             }
             bool ok = true;
@@ -714,9 +687,7 @@ tc_ffn_decode_kernel(const __grid_constant__ CUtensorMap tmW1, const __grid_cons
         }
         if (p.out != nullptr) {
             // ------------------------------------------------------------ combine
-            bool ok = true;
-            if (lane == 0) ok = wait_count(p.fc2_done, 4 * (U - U1), abort_flag);
-            if (__shfl_sync(0xffffffffu, ok, 0)) {
+            if (wait_count_warp(p.fc2_done, 4 * (U - U1), abort_flag, kWaitLimitNs, lane)) {
                 const int nvec = p.H / 8;
                 const long long total = static_cast<long long>(p.T) * nvec;
                 const int et = (warp - 2) * 32 + lane;   // 0..127

@@ -73,6 +73,46 @@ __device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, vo
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, limit_ns));
 }
 
+// ---------------------------------------------------------------- counters in global memory
+
+__device__ __forceinline__ int ld_acquire(const int32_t* p) {
+    int v;
+    asm volatile("ld.acquire.gpu.global.b32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+    return v;
+}
+
+// Bounded wait for *ctr >= target, by one lane; gives up as mbar_wait does.
+__device__ __forceinline__ bool wait_count(const int32_t* ctr, int target, volatile int* abort,
+                                           uint64_t limit_ns) {
+    if (ld_acquire(ctr) >= target) return true;
+    const uint64_t t0 = global_timer_ns();
+    for (;;) {
+        __nanosleep(64);
+        if (ld_acquire(ctr) >= target) return true;
+        if (*abort) return false;
+        if (global_timer_ns() - t0 > limit_ns) {
+            *abort = 1;
+            return false;
+        }
+    }
+}
+
+// The same for a whole warp, whose lanes then read what the counter stands for: the shuffle
+// alone orders no memory, the barrier behind it does.
+__device__ __forceinline__ bool wait_count_warp(const int32_t* ctr, int target, volatile int* abort,
+                                                uint64_t limit_ns, int lane) {
+    bool ok = true;
+    if (lane == 0) ok = wait_count(ctr, target, abort, limit_ns);
+    ok = __shfl_sync(0xffffffffu, ok, 0);
+    __syncwarp();
+    return ok;
+}
+
+// Orders this thread's accesses to global memory with those of the TMA unit.
+__device__ __forceinline__ void fence_proxy_async_global() {
+    asm volatile("fence.proxy.async.global;" ::: "memory");
+}
+
 // ---------------------------------------------------------------- TMA
 
 __device__ __forceinline__ void tma_prefetch_desc(const CUtensorMap* map) {
