@@ -15,8 +15,8 @@
 // adds each sequence's slots in order: no floating-point atomics, the same bits every time.
 // A batch that one block holds as one sequence is finished in the first launch.
 //
-// Batches of one sequence have kernels of their own (RAGGED false): the walk costs registers,
-// 131071 x 256 43 us forward instead of 41.
+// Batches of one sequence have kernels of their own (RAGGED false) without the walk (131071 x 256
+// 38.2 us forward instead of 39.1, 64 tokens 3.4 instead of 3.6).
 //
 // A row's E logits are spread over LPR lanes with 8 each (two 16-byte vectors where E is a
 // multiple of 4), 32 / LPR rows to a warp, the loads of the next two rows issued before the
@@ -49,20 +49,31 @@ __device__ __forceinline__ int seq_offset(const int32_t* seq, int s, int T) {
     return seq ? min(max(seq[s], 0), T) : (s == 0 ? 0 : T);
 }
 
-// First i with M_i >= t (the first offset that is), S + 1 if there is none; by the whole block.
-__device__ __forceinline__ int first_bound(const int32_t* seq, int S, int t, int T, int* s_first) {
-    if (t <= 0) return 0;
-    if (!seq) return t <= T ? 1 : 2;
+// First i >= from with M_i > t (the first offset that is), S + 1 if there is none; by the whole
+// block.  A search of every offset, not by halves: they may decrease.
+__device__ __forceinline__ int first_behind(const int32_t* seq, int S, int from, int t, int T, int* s_first) {
+    int at = S + 1;
+    if (S < 32) {   // every warp by itself
+        const int i = static_cast<int>(threadIdx.x) & 31;
+        const unsigned hits = __ballot_sync(0xffffffffu, i >= from && i <= S && seq_offset(seq, min(i, S), T) > t);
+        return hits ? __ffs(hits) - 1 : S + 1;
+    }
     if (threadIdx.x == 0) *s_first = S + 1;
     __syncthreads();
-    int at = S + 1;
-#pragma unroll 4
-    for (int i = threadIdx.x; i <= S; i += blockDim.x)
-        if (seq_offset(seq, i, T) >= t) at = min(at, i);
+    constexpr int kBatch = 16;   // loads in flight; most searches need one
+    for (int i0 = from + threadIdx.x; i0 <= S && at > S; i0 += kBatch * blockDim.x) {
+#pragma unroll
+        for (int u = kBatch - 1; u >= 0; --u) {
+            const int i = i0 + u * static_cast<int>(blockDim.x);
+            if (i <= S && seq_offset(seq, i, T) > t) at = i;
+        }
+    }
     at = __reduce_min_sync(0xffffffffu, at);
     if ((threadIdx.x & 31) == 0 && at <= S) atomicMin(s_first, at);
     __syncthreads();
-    return *s_first;
+    at = *s_first;
+    __syncthreads();   // it may be searched again
+    return at;
 }
 
 // The 8 logits of lane l (of LPR) of a row: with VEC, experts 4 l .. 4 l + 3 and
@@ -136,7 +147,7 @@ struct BalanceParams {
     const int32_t* seq;
     int T, E, k, S, per_block, blocks;
     float coef;
-    int32_t* bounds;       // [S + 1], M above; not used without seq
+    int32_t* bad;          // are the sequence offsets not their own M?
     float* part_p;         // [blocks + S, E]
     int32_t* part_c;       // [blocks + S, E]
     int32_t* part_n;       // [blocks + S]
@@ -185,42 +196,40 @@ balance_partial_kernel(const BalanceParams p) {
     pdl_trigger();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int l = lane & (LPR - 1), sub = lane / LPR;
-    const int b = blockIdx.x, E = p.E, T = p.T, S = p.S;
+    const int b = blockIdx.x, E = p.E, T = p.T, S = RAGGED ? p.S : 1;
     if (b == 0) {
         if (threadIdx.x == 0) *p.ticket = 0;
-        if (RAGGED && p.err) {
+        if (RAGGED) {
             // reported, not trusted: every use below is clamped
             bool bad = threadIdx.x == 0 && p.seq[0] != 0;
             for (int s = threadIdx.x; s < S; s += kBThreads)
                 bad = bad || p.seq[s + 1] < p.seq[s] || p.seq[s + 1] > T;
-            if (bad) atomicOr(p.err, kErrBadExpert);
+            bad = __syncthreads_or(bad);
+            if (threadIdx.x == 0) {
+                *p.bad = bad;
+                if (bad && p.err) atomicOr(p.err, kErrBadExpert);
+            }
         }
     }
     const int t0 = static_cast<int>(min(static_cast<long long>(b) * p.per_block, static_cast<long long>(T)));
     const int t1 = static_cast<int>(min(static_cast<long long>(t0) + p.per_block, static_cast<long long>(T)));
     const bool single = p.blocks <= 1 && S == 1;   // one block finishes the batch
-    // The walk starts with the sequence before the first bound in the range (its own bound is
-    // smaller: lo = t0 stands for it).
-    const int i0 = RAGGED ? first_bound(p.seq, S, t0, T, &s_first) : 0;
-    int lo = RAGGED && i0 == 0 ? seq_offset(p.seq, 0, T) : t0;
-    if (RAGGED && !single) {
-        // every bound is written by the block that holds it, those at T by the last block
-        int i = i0, m = lo;
-        for (; i <= S && m < t1; ++i) {
-            m = max(m, seq_offset(p.seq, i, T));
-            if (m < t1 && threadIdx.x == 0) p.bounds[i] = m;
-        }
-        if (b == static_cast<int>(gridDim.x) - 1 && m >= t1)
-            for (i = max(i - 1, 0) + threadIdx.x; i <= S; i += kBThreads) p.bounds[i] = T;
-    }
-    for (int s = RAGGED ? max(i0 - 1, 0) : 0; s < S; ++s) {
+    // The walk starts with token t0's sequence, the one before the first bound behind t0 (its
+    // own bound is at or before t0: lo = t0 stands for it).
+    const int i1 = RAGGED ? first_behind(p.seq, S, 0, t0, T, &s_first) : 1;
+    int lo = RAGGED && i1 == 0 ? seq_offset(p.seq, 0, T) : t0, empty = 0;
+    for (int s = single ? 0 : max(i1 - 1, 0); s < S; ++s) {
         int a = t0, z = t1;
         if (RAGGED) {
             if (lo >= t1 && !single) break;
             a = max(lo, t0);
             lo = max(lo, seq_offset(p.seq, s + 1, T));
             z = min(lo, t1);
-            if (a >= z && !single) continue;
+            if (a >= z && !single) {
+                // over a long run of empty sequences in one search
+                if (++empty % 16 == 0) s = first_behind(p.seq, S, s + 1, lo, T, &s_first) - 2;
+                continue;
+            }
         }
         for (int e = threadIdx.x; e < E; e += kBThreads) s_c[e] = 0;
         if (threadIdx.x == 0) s_n = 0;
@@ -248,28 +257,32 @@ balance_partial_kernel(const BalanceParams p) {
         r.load(row(t), E, l, t < z);
         next.load(row(t + kStep), E, l, t + kStep < z);
         const int trips = (z - a - warp * kRows + kStep - 1) / kStep;   // of this warp
-        for (int it = 0; it < trips; ++it) {
-            const uint8_t m2 = mask_of(t + 2 * kStep);
-            next2.load(row(t + 2 * kStep), E, l, t + 2 * kStep < z);
-            const bool live = t < z && m != 0;
-            r.softmax();   // a row past the end holds -inf: zeros
+        for (int it0 = 0; it0 < trips; it0 += kFold) {
+            const int end = min(it0 + kFold, trips);
+#pragma unroll 1
+            for (int it = it0; it < end; ++it) {
+                const uint8_t m2 = mask_of(t + 2 * kStep);
+                next2.load(row(t + 2 * kStep), E, l, t + 2 * kStep < z);
+                const bool live = t < z && m != 0;
+                r.softmax();   // a row past the end holds -inf: zeros
 #pragma unroll
-            for (int i = 0; i < kPer; ++i) acc[i] += live ? r.v[i] : 0.f;
-            n += live && l == 0;
-            t += kStep;
-            m = m1;
-            m1 = m2;
-            r = next;
-            next = next2;
-            if (it % kFold == kFold - 1) {
+                for (int i = 0; i < kPer; ++i) acc[i] += live ? r.v[i] : 0.f;
+                n += live && l == 0;
+                t += kStep;
+                m = m1;
+                m1 = m2;
+                r = next;
+                next = next2;
+            }
+            if (end < trips) {
 #pragma unroll
                 for (int i = 0; i < kPer; ++i) {
-                    s_p[warp][32 * i + lane] = (it < kFold ? 0.f : s_p[warp][32 * i + lane]) + acc[i];
+                    s_p[warp][32 * i + lane] = (it0 == 0 ? 0.f : s_p[warp][32 * i + lane]) + acc[i];
                     acc[i] = 0.f;
                 }
             }
         }
-        if (trips >= kFold) {
+        if (trips > kFold) {
 #pragma unroll
             for (int i = 0; i < kPer; ++i) acc[i] += s_p[warp][32 * i + lane];
             __syncwarp();
@@ -331,7 +344,20 @@ balance_reduce_kernel(const BalanceParams p) {
     __syncthreads();
     const int s = blockIdx.x, E = p.E, nb = gridDim.y;
     const int e = static_cast<int>(blockIdx.y) * kRExperts + (threadIdx.x & 31), st = threadIdx.x >> 5;
-    const int lo = p.seq ? p.bounds[s] : 0, hi = p.seq ? p.bounds[s + 1] : p.T;
+    int lo = 0, hi = p.T;
+    if (p.seq) {
+        lo = seq_offset(p.seq, s, p.T);
+        hi = seq_offset(p.seq, s + 1, p.T);
+        if (*p.bad) {   // M_s and M_{s+1}
+            for (int i = threadIdx.x; i < s; i += kBThreads) lo = max(lo, seq_offset(p.seq, i, p.T));
+            lo = __reduce_max_sync(0xffffffffu, lo);
+            if ((threadIdx.x & 31) == 0) s_cnt[threadIdx.x >> 5] = lo;
+            __syncthreads();
+            for (int i = 0; i < kBWarps; ++i) lo = max(lo, s_cnt[i]);
+            __syncthreads();
+            hi = max(lo, hi);
+        }
+    }
     const int b0 = lo / p.per_block, b1 = hi > lo ? (hi - 1) / p.per_block + 1 : b0;
     int n = 0;
     for (int b = b0 + threadIdx.x; b < b1; b += kBThreads) n += p.part_n[b + s];
@@ -391,10 +417,9 @@ balance_grad_kernel(const BalanceGradArgs a, int per_block) {
     const int t1 = static_cast<int>(min(static_cast<long long>(t0) + per_block, static_cast<long long>(T)));
     int t = t0 + warp * kRows + sub;
     // the lane group's sequence: its bounds (M), shares less 1/E and scale; t only grows.  It
-    // starts with the block's first token: the sequence before the first bound behind t0
-    // (whose own bound is at or before t0: lo = t0 stands for it), or none.
+    // starts with the block's first token, as the forward's walk does.
     __shared__ int s_first;
-    const int i1 = first_bound(a.seq_offsets, a.S, t0 + 1, T, &s_first);
+    const int i1 = !a.seq_offsets ? 1 : first_behind(a.seq_offsets, a.S, 0, t0, T, &s_first);
     int s = min(max(i1 - 1, 0), a.S - 1);
     int lo = i1 == 0 ? seq_offset(a.seq_offsets, 0, T) : t0;
     int hi = i1 > a.S ? t0 : max(lo, seq_offset(a.seq_offsets, s + 1, T));
@@ -456,7 +481,7 @@ size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
 struct BalanceLayout {
     int blocks, per_block;
-    size_t ticket, bounds, seq_loss, part_n, part_c, part_p, total;
+    size_t ticket, bad, seq_loss, part_n, part_c, part_p, total;
 };
 
 // Lanes of a row: the smallest power of two that holds E logits at 8 a lane.
@@ -485,8 +510,8 @@ BalanceLayout balance_layout(int T, int E, int S) {
     const int finest = (T + kTokensPerBlockMin - 1) / kTokensPerBlockMin;
     const size_t slots = static_cast<size_t>(finest < most ? finest : most) + S;
     L.ticket = 0;
-    L.bounds = 256;
-    L.seq_loss = L.bounds + align256((static_cast<size_t>(S) + 1) * 4);
+    L.bad = 4;
+    L.seq_loss = 256;
     L.part_n = L.seq_loss + align256(static_cast<size_t>(S) * ((E + kRExperts - 1) / kRExperts) * 8);
     L.part_c = L.part_n + align256(slots * 4);
     L.part_p = L.part_c + align256(slots * E * 4);
@@ -520,7 +545,7 @@ cudaError_t launch_balance_loss(const BalanceArgs& a, cudaStream_t s) {
     const BalanceLayout L = balance_layout(a.T, a.E, a.S);
     char* ws = static_cast<char*>(a.workspace);
     const BalanceParams p{a.logits, a.topk_idx, a.mask, a.seq_offsets, a.T, a.E, a.k, a.S, L.per_block, L.blocks,
-                          a.coef, reinterpret_cast<int32_t*>(ws + L.bounds), reinterpret_cast<float*>(ws + L.part_p), reinterpret_cast<int32_t*>(ws + L.part_c),
+                          a.coef, reinterpret_cast<int32_t*>(ws + L.bad), reinterpret_cast<float*>(ws + L.part_p), reinterpret_cast<int32_t*>(ws + L.part_c),
                           reinterpret_cast<int32_t*>(ws + L.part_n), reinterpret_cast<int32_t*>(ws + L.ticket),
                           reinterpret_cast<double*>(ws + L.seq_loss), a.loss, a.counts, a.probs, a.tokens, a.err};
     const dim3 grid(L.blocks > 0 ? L.blocks : 1), block(kBThreads);

@@ -153,3 +153,17 @@ def test_blocks_of_many_rows(E, S, masked):
     assert torch.all(over <= 0), (float(over.max()), int(over.argmax()) // E)
     again = moe.balance_loss(lg, idx, coef=0.01, mask=mask, seq_offsets=s)
     assert all(torch.equal(again[a], r[a]) for a in r)
+
+
+@pytest.mark.parametrize("T", [90, 1500])
+def test_long_runs_of_empty_sequences_between_others(T):
+    """Runs of 15 to 1100 empty sequences inside a block, at its ends and at the batch's, some
+    of them by offsets that decrease."""
+    lg, idx, rng = batch(T, 8, 2, T)
+    seq = [0] * 17
+    for at, times in ((3, 15), (4, 16), (64, 33), (66, 1100), (min(T - 5, 512), 31), (T - 2, 40), (T, 20)):
+        seq += [at] * times
+    for s in (seq, [v - (i % 7 == 3) * min(v, 2) for i, v in enumerate(seq)]):
+        bounds = np.maximum.accumulate(np.clip(s, 0, T))
+        got = run(lg, idx, 1.0, None, s, workspace=poisoned(T, 8, len(s) - 1))
+        compare(got, lg, idx, 1.0, None, bounds)
